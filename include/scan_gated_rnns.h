@@ -112,7 +112,12 @@ typedef enum sgr_status {
                                  outputs are NaN.  Reported by sgr_workspace_status */
 } sgr_status_t;
 
-typedef enum sgr_dtype { SGR_F32 = 0, SGR_BF16 = 1 } sgr_dtype_t;
+/* SGR_F16 and SGR_I8: the gated recurrence and the 8-bit projection only (the
+ * other entry points refuse them). */
+typedef enum sgr_dtype { SGR_F32 = 0, SGR_BF16 = 1, SGR_F16 = 2, SGR_I8 = 3 } sgr_dtype_t;
+
+/* Gate of gated_scan, gated_scan_backward and gated_step. */
+typedef enum sgr_gate { SGR_GATE_SIGMOID = 0, SGR_GATE_LOG = 1 } sgr_gate_t;
 
 /* SGR_OP_MINGRU_LOG names mingru_scan_log for sgr_workspace_size and
  * sgr_scan_plan only (it has no gradient, summary or step entry points). */
@@ -577,6 +582,117 @@ SGR_API int sgr_backward_kernel(sgr_op_t op, int64_t B, int64_t T, int64_t D, sg
  */
 SGR_API sgr_status_t sgr_set_wait_limit(uint32_t polls);
 SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
+
+/* ------------------------------------------ gated linear recurrence */
+
+/*
+ * gated_scan -- the gated linear recurrence over packed sequences:
+ *     SGR_GATE_SIGMOID: a_t = sigmoid(f_t),      h_t = a_t h_{t-1} + (1 - a_t) v_t
+ *     SGR_GATE_LOG:     a_t = exp(min(f_t, 0)),  h_t = a_t h_{t-1} + v_t
+ * element-wise over D channels, values of either sign (minGRU without its
+ * positive candidate; a free decay for long memories).
+ *
+ *   f, v       : (rows, D) in dtype (SGR_F32, SGR_BF16 or SGR_F16), unit stride
+ *                along D, any row stride (elements): the two halves of one
+ *                projection's output are read in place.
+ *   cu_seqlens : n_seqs + 1 ascending row bounds on the device, cu_bytes 4 or 8
+ *                each; sequence s holds rows cu[s] .. cu[s+1]-1 and may be
+ *                empty.  NULL: n_seqs sequences of rows / n_seqs rows each.
+ *                Rows before cu[0] or from cu[n_seqs] on belong to no sequence
+ *                (padding): h is 0 there if zero_padding, else left as it was.
+ *                The bounds are not checked (they lie on the device); others
+ *                than ascending ones give unspecified values, and no access
+ *                outside the arrays.
+ *   h0         : fp32 initial states, row s h0_seq_stride elements apart (0: one
+ *                state for every sequence); NULL: 0.
+ *   h          : (rows, D) in dtype.  h_last: fp32 (n_seqs, D), the state behind
+ *                each sequence (h0 where it is empty), or NULL.
+ *   states     : fp32 (sgr_gated_chunks(rows), D): the state entering every
+ *                chunk of rows, what gated_scan_backward starts from (the row of
+ *                a chunk that begins with a sequence is not written), or NULL.
+ *   workspace  : sgr_gated_workspace_size(rows, D) bytes; need not be
+ *                initialised and keeps nothing from call to call.  Not to be
+ *                shared with another call that can run at the same time, nor
+ *                with the entry points that keep hand-off words in theirs.
+ * States and arithmetic are fp32.  A NaN or infinity stays within its sequence
+ * and channel.  The result does not depend on how blocks are timed: equal
+ * calls give equal bits.  Calls may be captured; a chunk that waited too long
+ * leaves NaN and sets the workspace's status word.
+ */
+SGR_API sgr_status_t gated_scan(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride,
+                                const float *h0, int64_t h0_seq_stride, const void *cu_seqlens, int cu_bytes,
+                                int64_t n_seqs, void *h, int64_t h_row_stride, float *h_last, float *states,
+                                int64_t rows, int64_t D, sgr_gate_t gate, sgr_dtype_t dtype, int zero_padding,
+                                void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * gated_scan_backward -- gradients through gated_scan.  With g_t = dh_t +
+ * a_{t+1} g_{t+1} within a sequence (its last row adds dh_last):
+ *     SGR_GATE_SIGMOID: dv = (1 - a) g,  df = a (1 - a) (h_{t-1} - v) g
+ *     SGR_GATE_LOG:     dv = g,          df = [f <= 0] a h_{t-1} g
+ *   states  : as gated_scan left them for the same f, v, h0 and bounds.
+ *   dh      : (rows, D) in dtype; dh_last: fp32 (n_seqs, D) or NULL (0).
+ *   df, dv  : (rows, D) in dtype; 0 at padding rows.
+ *   dh0     : fp32 (n_seqs, D), or NULL; the caller sums it over the sequences
+ *             where one state served them all.
+ */
+SGR_API sgr_status_t gated_scan_backward(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride,
+                                         const float *h0, int64_t h0_seq_stride, const void *cu_seqlens,
+                                         int cu_bytes, int64_t n_seqs, const float *states, const void *dh,
+                                         int64_t dh_row_stride, const float *dh_last, void *df,
+                                         int64_t df_row_stride, void *dv, int64_t dv_row_stride, float *dh0,
+                                         int64_t rows, int64_t D, sgr_gate_t gate, sgr_dtype_t dtype,
+                                         void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of workspace of the two calls above (0: none needed, also for sizes they refuse). */
+SGR_API size_t sgr_gated_workspace_size(int64_t rows, int64_t D);
+
+/* Rows of `states` for `rows` rows. */
+SGR_API int64_t sgr_gated_chunks(int64_t rows);
+
+/*
+ * gated_step -- one token for each of `rows` requests: with s = slots[i],
+ *     state[s] = a_i state[s] + b_i   (a, b as above),   h[i] = state[s].
+ *   state : fp32 (n_slots, D), rows state_row_stride apart, updated in place.
+ *   slots : `rows` slot numbers on the device, slot_bytes 4 or 8 each; NULL:
+ *           row i has slot i.  Rows whose slot is negative or at least n_slots
+ *           are padding: h is 0 there if zero_padding, else left as it was.  A
+ *           slot that several rows name takes their tokens in row order.
+ *   h     : (rows, D) in dtype; must not overlap f, v or state.
+ */
+SGR_API sgr_status_t gated_step(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride, float *state,
+                                int64_t state_row_stride, int64_t n_slots, const void *slots, int slot_bytes, void *h,
+                                int64_t h_row_stride, int64_t rows, int64_t D, sgr_gate_t gate, sgr_dtype_t dtype,
+                                int zero_padding, cudaStream_t stream);
+
+/* ------------------------------------------------- 8-bit projection */
+
+/*
+ * int8_quantize -- rows of x (rows, K) as whole numbers and one scale each:
+ * scale = max |x| / 127 (at least 2^-100), q = x / scale to the nearest whole
+ * number (ties to even), decided on the exact quotient.  A row with an infinity
+ * or NaN gets the scale NaN and q = 0.  Serves tokens and weights' channels.
+ */
+SGR_API sgr_status_t int8_quantize(const void *x, int64_t x_row_stride, int8_t *q, int64_t q_row_stride, float *scale,
+                                   int64_t rows, int64_t K, sgr_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * int8_projection -- y[m, n] = (sum_k q_x[m, k] w[n, k]) x_scale[m] w_scale[n] + bias[n],
+ * the sum exact in int32 (1 <= K < 2^17).
+ *   x       : (rows, K) of x_dtype: SGR_I8 with its scales x_scale (rows), or a
+ *             floating type with x_scale NULL, whose rows are quantised as by
+ *             int8_quantize within the call.
+ *   w       : (N, K) signed 8-bit, w_scale fp32 (N), bias fp32 (N) or NULL.
+ *   y       : (rows, N) of y_dtype (SGR_F32, SGR_BF16 or SGR_F16).
+ * Strides are in elements.  w (and 8-bit x) whose rows start on 16-byte
+ * boundaries take the tensor-core kernel, others a slower one.
+ *   workspace: sgr_int8_workspace_size(rows, K, x_dtype) bytes, uninitialised.
+ */
+SGR_API sgr_status_t int8_projection(const void *x, int64_t x_row_stride, sgr_dtype_t x_dtype, const float *x_scale,
+                                     const int8_t *w, int64_t w_row_stride, const float *w_scale, const float *bias,
+                                     void *y, int64_t y_row_stride, sgr_dtype_t y_dtype, int64_t rows, int64_t K,
+                                     int64_t N, void *workspace, size_t ws_bytes, cudaStream_t stream);
+SGR_API size_t sgr_int8_workspace_size(int64_t rows, int64_t K, sgr_dtype_t x_dtype);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,11 @@ SGR_ERR_TIMEOUT = 5
 
 SGR_F32 = 0
 SGR_BF16 = 1
+SGR_F16 = 2
+SGR_I8 = 3
+
+SGR_GATE_SIGMOID = 0
+SGR_GATE_LOG = 1
 
 SGR_OP_MINGRU = 0
 SGR_OP_MINMAX = 1
@@ -89,6 +94,21 @@ SIGNATURES.update({
                                           _vp]),
     "mingru_scan_host": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _int, _int, _vp, _sz, _vp]),
     "minmax_scan_host": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _int, _int, _vp, _sz, _vp]),
+})
+
+SIGNATURES.update({
+    "gated_scan": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _int,
+                          _int, _int, _vp, _sz, _vp]),
+    "gated_scan_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                                   _vp, _i64, _vp, _i64, _i64, _int, _int, _vp, _sz, _vp]),
+    "sgr_gated_workspace_size": (_sz, [_i64, _i64]),
+    "sgr_gated_chunks": (_i64, [_i64]),
+    "gated_step": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _int, _vp, _i64, _i64, _i64, _int, _int, _int,
+                          _vp]),
+    "int8_quantize": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp]),
+    "int8_projection": (_int, [_vp, _i64, _int, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _int, _i64, _i64, _i64, _vp,
+                               _sz, _vp]),
+    "sgr_int8_workspace_size": (_sz, [_i64, _i64, _int]),
 })
 
 KERNEL_TILE = 1

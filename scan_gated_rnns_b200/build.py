@@ -24,7 +24,7 @@ STEP_EXE = os.path.join(PKG, "step_latency")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
          "-Xcompiler", "-fvisibility=hidden",
-         "--expt-relaxed-constexpr", "-Xcompiler", "-Wall"]
+         "--expt-relaxed-constexpr", "--threads", "0", "-Xcompiler", "-Wall"]
 
 
 def nvcc() -> str:
@@ -39,7 +39,7 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:

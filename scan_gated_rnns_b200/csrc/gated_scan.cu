@@ -1,0 +1,242 @@
+// gated_scan.cu -- host side of gated_scan, gated_scan_backward and
+// gated_step (include/scan_gated_rnns.h): argument checks, the choice of
+// kernel, the workspace and the launches.  No allocation, no synchronisation.
+#include "gated_scan.cuh"
+#include "gated_step.cuh"
+#include "host_checks.h"
+
+#include <algorithm>
+#include <cstring>
+#include <limits>
+
+namespace {
+
+using namespace sgr;
+using namespace sgr::gated;
+using sgr::host::Span;
+
+constexpr size_t kHeader = 256;             // status word at 0, ticket at 64
+constexpr size_t kTicketAt = 64;
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1 - kTR;
+constexpr int kBlocksPerSM = 2;
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Workspace: header, flags, maps, and the carried states (forward calls that
+// keep no states, and every backward call).
+struct Layout {
+    int64_t n_strips, n_chunks, n_tiles;
+    size_t flags, maps, carry, total;
+};
+Layout layout(int64_t rows, int64_t D, int tc) {
+    Layout l;
+    l.n_strips = (D + tc - 1) / tc;
+    l.n_chunks = (rows + kTR - 1) / kTR;
+    l.n_tiles = l.n_strips * l.n_chunks;
+    l.flags = kHeader;
+    l.maps = align_up(l.flags + size_t(l.n_tiles) * 4, 256);
+    l.carry = align_up(l.maps + size_t(l.n_tiles) * tc * 8, 256);
+    l.total = align_up(l.carry + size_t(l.n_chunks) * size_t(D) * 4, 256);
+    return l;
+}
+
+bool sizes_ok(int64_t rows, int64_t D) {
+    int64_t n = 0;
+    // 16 bytes an element covers the workspace and every dense array
+    return rows <= kMaxRows && D <= (int64_t(1) << 31) - 64 && host::mul_ok(rows, D, &n) && host::mul_ok(n, 16, &n) &&
+           ((rows + kTR - 1) / kTR) * ((D + 31) / 32) <= std::numeric_limits<int>::max();
+}
+
+template <typename IO, int E, int GATE>
+cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int sms = host::sm_count(dev);
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int64_t most = p.ticket ? int64_t(sms) * kBlocksPerSM : p.n_tiles;
+    const unsigned grid = unsigned(std::max<int64_t>(1, std::min(p.n_tiles, most)));
+    if (backward) gated_scan_backward_kernel<IO, E, GATE><<<grid, kThreads, 0, s>>>(p);
+    else gated_scan_kernel<IO, E, GATE><<<grid, kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename IO, int E>
+cudaError_t launch_gate(const GatedParams &p, int gate, bool backward, cudaStream_t s) {
+    return gate == GATE_SIGMOID ? launch<IO, E, GATE_SIGMOID>(p, backward, s) : launch<IO, E, GATE_LOG>(p, backward, s);
+}
+
+cudaError_t launch_any(const GatedParams &p, sgr_dtype_t dtype, int gate, int E, bool backward, cudaStream_t s) {
+    if (dtype == SGR_F32) return launch_gate<float, 1>(p, gate, backward, s);
+    if (dtype == SGR_BF16)
+        return E == 2 ? launch_gate<__nv_bfloat16, 2>(p, gate, backward, s)
+                      : launch_gate<__nv_bfloat16, 1>(p, gate, backward, s);
+    return E == 2 ? launch_gate<__half, 2>(p, gate, backward, s) : launch_gate<__half, 1>(p, gate, backward, s);
+}
+
+sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backward, void *ws, size_t ws_bytes,
+                 cudaStream_t stream) {
+    const int esz = host::float_size(dtype);
+    if (esz == 0 || (gate != SGR_GATE_SIGMOID && gate != SGR_GATE_LOG)) return SGR_ERR_INVALID_ARG;
+    if (p.rows < 0 || p.D < 0 || p.n_seqs < 0 || p.h0_ss < 0) return SGR_ERR_INVALID_ARG;
+    if (p.cu ? (p.cu_bytes != 4 && p.cu_bytes != 8) : (p.rows > 0 && (p.n_seqs == 0 || p.rows % p.n_seqs != 0)))
+        return SGR_ERR_INVALID_ARG;
+    if (p.D == 0 || (p.rows == 0 && p.n_seqs == 0)) return SGR_OK;
+    if (p.f_rs < 0 || p.v_rs < 0 || p.h_rs < 0 || p.dh_rs < 0 || p.df_rs < 0 || p.dv_rs < 0) return SGR_ERR_INVALID_ARG;
+    if (!sizes_ok(p.rows, p.D) || p.n_seqs > std::numeric_limits<int>::max()) return SGR_ERR_UNSUPPORTED;
+    const int64_t n_chunks = (p.rows + kTR - 1) / kTR;
+    if (p.rows > 0) {
+        if (!p.f || !p.v) return SGR_ERR_INVALID_ARG;
+        if (backward ? (!p.dh || !p.df || !p.dv || (n_chunks > 1 && !p.states)) : !p.h) return SGR_ERR_INVALID_ARG;
+        // written rows may not share elements with one another
+        if (p.rows > 1 && (backward ? (p.df_rs < p.D || p.dv_rs < p.D) : p.h_rs < p.D)) return SGR_ERR_INVALID_ARG;
+    }
+    int64_t b_f, b_v, b_dh, b_h, b_df, b_dv, b_h0, b_seq, b_cu, b_st;
+    if (!host::span_ok(p.rows, p.D, p.f_rs, esz, &b_f) || !host::span_ok(p.rows, p.D, p.v_rs, esz, &b_v) ||
+        !host::span_ok(p.rows, p.D, p.dh_rs, esz, &b_dh) || !host::span_ok(p.rows, p.D, p.h_rs, esz, &b_h) ||
+        !host::span_ok(p.rows, p.D, p.df_rs, esz, &b_df) || !host::span_ok(p.rows, p.D, p.dv_rs, esz, &b_dv) ||
+        !host::span_ok(p.n_seqs, p.D, p.h0_ss, 4, &b_h0) || !host::span_ok(p.n_seqs, p.D, p.D, 4, &b_seq) ||
+        !host::mul_ok(p.n_seqs + 1, p.cu_bytes, &b_cu) || !host::span_ok(n_chunks, p.D, p.D, 4, &b_st))
+        return SGR_ERR_UNSUPPORTED;
+    // Two channels a thread where every row starts on a 4-byte boundary.
+    int E = 1;
+    if (esz == 2) {
+        const int64_t odd = p.D | (p.rows > 1 ? (p.f_rs | p.v_rs | p.dh_rs | p.h_rs | p.df_rs | p.dv_rs) : 0);
+        bool four = true;
+        for (const void *q : {p.f, p.v, p.dh, static_cast<const void *>(p.h), static_cast<const void *>(p.df),
+                              static_cast<const void *>(p.dv)})
+            four = four && host::aligned(q, 4);
+        E = (odd & 1) == 0 && four ? 2 : 1;
+    }
+    const Layout l = layout(p.rows, p.D, 32 * E);
+    p.n_strips = l.n_strips;
+    p.n_chunks = l.n_chunks;
+    p.n_tiles = l.n_tiles;
+    p.seq_rows = p.cu ? 1u : uint32_t(p.rows / std::max<int64_t>(1, p.n_seqs));
+    p.spin_limit = kSpinLimit;
+    Span out[4], in[8];
+    if (backward) {
+        out[0] = {p.df, b_df};
+        out[1] = {p.dv, b_dv};
+        out[2] = {p.dh0, b_seq};
+        out[3] = {ws, p.n_chunks > 1 ? int64_t(l.total) : 0};
+    } else {
+        out[0] = {p.h, b_h};
+        out[1] = {p.h_last, b_seq};
+        out[2] = {p.states, b_st};
+        out[3] = {ws, p.n_chunks > 1 ? int64_t(l.total) : 0};
+    }
+    const Span ins[8] = {{p.f, b_f}, {p.v, b_v}, {p.dh, b_dh}, {p.h0, b_h0}, {p.dh_last, b_seq}, {p.cu, b_cu},
+                         {backward ? p.states : nullptr, b_st}, {nullptr, 0}};
+    std::copy(ins, ins + 8, in);
+    if (host::any_overlap(out, in)) return SGR_ERR_INVALID_ARG;
+    if (p.n_chunks > 1) {
+        if (!ws || ws_bytes < l.total || !host::aligned(ws, 16)) return SGR_ERR_WORKSPACE;
+        char *w = static_cast<char *>(ws);
+        p.status = reinterpret_cast<uint32_t *>(w);
+        p.ticket = reinterpret_cast<uint32_t *>(w + kTicketAt);
+        p.flags = reinterpret_cast<uint32_t *>(w + l.flags);
+        p.maps = reinterpret_cast<float2 *>(w + l.maps);
+        p.carry = reinterpret_cast<float *>(w + l.carry);
+        if (!backward && !p.states) p.states = p.carry;
+        // nothing of an earlier call is read: status, ticket and flags are cleared on the stream
+        if (cudaMemsetAsync(w, 0, l.maps, stream) != cudaSuccess) return SGR_ERR_CUDA;
+    }
+    return launch_any(p, dtype, gate == SGR_GATE_LOG ? GATE_LOG : GATE_SIGMOID, E, backward, stream) == cudaSuccess
+               ? SGR_OK
+               : SGR_ERR_CUDA;
+}
+
+template <typename IO, int V>
+void launch_step(const StepParams &p, int gate, unsigned grid, cudaStream_t s) {
+    if (gate == SGR_GATE_SIGMOID) gated_step_kernel<IO, GATE_SIGMOID, V><<<grid, 256, 0, s>>>(p);
+    else gated_step_kernel<IO, GATE_LOG, V><<<grid, 256, 0, s>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sgr_gated_chunks(int64_t rows) { return rows <= 0 ? 0 : (rows + kTR - 1) / kTR; }
+
+size_t sgr_gated_workspace_size(int64_t rows, int64_t D) {
+    if (rows <= kTR || D <= 0 || !sizes_ok(rows, D)) return 0;
+    return std::max(layout(rows, D, 32).total, layout(rows, D, 64).total);
+}
+
+sgr_status_t gated_scan(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride, const float *h0,
+                        int64_t h0_seq_stride, const void *cu_seqlens, int cu_bytes, int64_t n_seqs, void *h,
+                        int64_t h_row_stride, float *h_last, float *states, int64_t rows, int64_t D, sgr_gate_t gate,
+                        sgr_dtype_t dtype, int zero_padding, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    GatedParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.f = f; p.f_rs = f_row_stride; p.v = v; p.v_rs = v_row_stride;
+    p.h0 = h0; p.h0_ss = h0 ? h0_seq_stride : 0;
+    p.cu = cu_seqlens; p.cu_bytes = cu_seqlens ? cu_bytes : 0; p.n_seqs = n_seqs;
+    p.h = h; p.h_rs = h_row_stride; p.h_last = h_last; p.states = states;
+    p.rows = rows; p.D = D; p.zero_padding = zero_padding;
+    return run(p, dtype, gate, false, workspace, ws_bytes, stream);
+}
+
+sgr_status_t gated_scan_backward(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride,
+                                 const float *h0, int64_t h0_seq_stride, const void *cu_seqlens, int cu_bytes,
+                                 int64_t n_seqs, const float *states, const void *dh, int64_t dh_row_stride,
+                                 const float *dh_last, void *df, int64_t df_row_stride, void *dv,
+                                 int64_t dv_row_stride, float *dh0, int64_t rows, int64_t D, sgr_gate_t gate,
+                                 sgr_dtype_t dtype, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    GatedParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.f = f; p.f_rs = f_row_stride; p.v = v; p.v_rs = v_row_stride;
+    p.h0 = h0; p.h0_ss = h0 ? h0_seq_stride : 0;
+    p.cu = cu_seqlens; p.cu_bytes = cu_seqlens ? cu_bytes : 0; p.n_seqs = n_seqs;
+    p.states = const_cast<float *>(states);
+    p.dh = dh; p.dh_rs = dh_row_stride; p.dh_last = dh_last;
+    p.df = df; p.df_rs = df_row_stride; p.dv = dv; p.dv_rs = dv_row_stride; p.dh0 = dh0;
+    p.rows = rows; p.D = D; p.zero_padding = 1;
+    return run(p, dtype, gate, true, workspace, ws_bytes, stream);
+}
+
+sgr_status_t gated_step(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride, float *state,
+                        int64_t state_row_stride, int64_t n_slots, const void *slots, int slot_bytes, void *h,
+                        int64_t h_row_stride, int64_t rows, int64_t D, sgr_gate_t gate, sgr_dtype_t dtype,
+                        int zero_padding, cudaStream_t stream) {
+    const int esz = host::float_size(dtype);
+    if (esz == 0 || (gate != SGR_GATE_SIGMOID && gate != SGR_GATE_LOG)) return SGR_ERR_INVALID_ARG;
+    if (rows < 0 || D < 0 || n_slots < 0 || f_row_stride < 0 || v_row_stride < 0 || h_row_stride < 0 ||
+        state_row_stride < 0)
+        return SGR_ERR_INVALID_ARG;
+    if (rows == 0 || D == 0) return SGR_OK;
+    if (!f || !v || !h || (n_slots > 0 && !state)) return SGR_ERR_INVALID_ARG;
+    if (slots ? (slot_bytes != 4 && slot_bytes != 8) : n_slots < rows) return SGR_ERR_INVALID_ARG;
+    if ((rows > 1 && h_row_stride < D) || (n_slots > 1 && state_row_stride < D)) return SGR_ERR_INVALID_ARG;
+    int64_t b_f, b_v, b_h, b_s, b_slots;
+    if (!host::span_ok(rows, D, f_row_stride, esz, &b_f) || !host::span_ok(rows, D, v_row_stride, esz, &b_v) ||
+        !host::span_ok(rows, D, h_row_stride, esz, &b_h) || !host::span_ok(n_slots, D, state_row_stride, 4, &b_s) ||
+        !host::mul_ok(rows, slots ? slot_bytes : 0, &b_slots))
+        return SGR_ERR_UNSUPPORTED;
+    const Span out[2] = {{h, b_h}, {state, b_s}}, in[3] = {{f, b_f}, {v, b_v}, {slots, b_slots}};
+    if (host::any_overlap(out, in)) return SGR_ERR_INVALID_ARG;
+    StepParams p;
+    p.f = f; p.f_rs = f_row_stride; p.v = v; p.v_rs = v_row_stride; p.h = h; p.h_rs = h_row_stride;
+    p.state = state; p.state_rs = state_row_stride; p.n_slots = n_slots; p.slots = slots; p.slot_bytes = slot_bytes;
+    p.rows = rows; p.D = D; p.zero_padding = zero_padding;
+    // four channels a thread where every row allows 16-byte states and 4-element operands
+    const int64_t strides = D | f_row_stride | v_row_stride | h_row_stride | state_row_stride;
+    const bool four = strides % 4 == 0 && host::aligned(f, 4 * esz) && host::aligned(v, 4 * esz) &&
+                      host::aligned(h, 4 * esz) && host::aligned(state, 16);
+    const int V = four ? 4 : 1;
+    p.d_blocks = (D + 256 * V - 1) / (256 * V);
+    int64_t grid = 0;
+    if (!host::mul_ok(rows, p.d_blocks, &grid) || grid > std::numeric_limits<int>::max()) return SGR_ERR_UNSUPPORTED;
+    if (dtype == SGR_F32) {
+        four ? launch_step<float, 4>(p, gate, unsigned(grid), stream) : launch_step<float, 1>(p, gate, unsigned(grid), stream);
+    } else if (dtype == SGR_BF16) {
+        four ? launch_step<__nv_bfloat16, 4>(p, gate, unsigned(grid), stream)
+             : launch_step<__nv_bfloat16, 1>(p, gate, unsigned(grid), stream);
+    } else {
+        four ? launch_step<__half, 4>(p, gate, unsigned(grid), stream) : launch_step<__half, 1>(p, gate, unsigned(grid), stream);
+    }
+    return cudaGetLastError() == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
+}
+
+}  // extern "C"

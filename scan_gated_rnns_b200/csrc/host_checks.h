@@ -1,0 +1,67 @@
+// host_checks.h -- argument checks shared by the host sides of the gated
+// recurrence and the 8-bit projection.
+#pragma once
+
+#include "scan_gated_rnns.h"
+
+#include <atomic>
+#include <cstddef>
+#include <cstdint>
+
+namespace sgr {
+namespace host {
+
+// a * b for sizes and strides, false if it passes int64
+inline bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
+
+inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// bytes that `rows` rows of n elements, rs elements apart, span from the first
+// to the last; false if they pass int64
+inline bool span_ok(int64_t rows, int64_t n, int64_t rs, int64_t esz, int64_t *bytes) {
+    int64_t x = 0;
+    if (rows <= 0 || n <= 0) {
+        *bytes = 0;
+        return true;
+    }
+    return mul_ok(rows - 1, rs, &x) && !__builtin_add_overflow(x, n, &x) && mul_ok(x, esz, bytes);
+}
+
+inline bool overlaps(const void *a, int64_t na, const void *b, int64_t nb) {
+    if (!a || !b || na <= 0 || nb <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
+}
+
+// An array of rows as a call gives it, with the bytes it spans.
+struct Span {
+    const void *p;
+    int64_t n;
+};
+template <int N, int M>
+inline bool any_overlap(const Span (&outs)[N], const Span (&ins)[M]) {
+    for (int i = 0; i < N; ++i) {
+        for (int j = 0; j < M; ++j)
+            if (overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return true;
+        for (int j = i + 1; j < N; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+    }
+    return false;
+}
+
+// SMs of a device; 0 if the runtime does not say
+inline int sm_count(int dev) {
+    static std::atomic<int> cache[64];
+    if (dev < 0 || dev >= 64) return 0;
+    int v = cache[dev].load();
+    if (v == 0) {
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) v = 0;
+        cache[dev].store(v);
+    }
+    return v;
+}
+
+inline int float_size(sgr_dtype_t t) { return t == SGR_F32 ? 4 : (t == SGR_BF16 || t == SGR_F16 ? 2 : 0); }
+
+}  // namespace host
+}  // namespace sgr

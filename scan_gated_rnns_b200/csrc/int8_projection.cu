@@ -1,0 +1,104 @@
+// int8_projection.cu -- host side of int8_quantize and int8_projection
+// (include/scan_gated_rnns.h): argument checks, the choice of kernel, the
+// workspace and the launches.  No allocation, no synchronisation.
+#include "host_checks.h"
+#include "int8_projection.cuh"
+
+#include <algorithm>
+#include <limits>
+
+namespace {
+
+using namespace sgr;
+using namespace sgr::i8;
+using sgr::host::Span;
+
+constexpr int64_t kMaxK = (int64_t(1) << 17) - 1;      // 128 * 128 * K stays below 2^31
+constexpr int64_t kMaxDim = std::numeric_limits<int>::max() - 4096;
+
+inline int64_t pad16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// Workspace of a product whose x is not 8-bit: the quantised rows, then their scales.
+size_t quant_bytes(int64_t M, int64_t K) { return size_t(M) * size_t(pad16(K)); }
+size_t scale_at(int64_t M, int64_t K) { return (quant_bytes(M, K) + 255) / 256 * 256; }
+
+sgr_status_t quantize(const QuantParams &p, sgr_dtype_t dtype, cudaStream_t s) {
+    const unsigned grid = unsigned(std::min<int64_t>(p.rows, 148 * 64));
+    if (dtype == SGR_F32) int8_quantize_kernel<float><<<grid, 256, 0, s>>>(p);
+    else if (dtype == SGR_BF16) int8_quantize_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+    else int8_quantize_kernel<__half><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
+}
+
+sgr_status_t product(const ProjectParams &p, sgr_dtype_t out, cudaStream_t s) {
+    const dim3 grid(unsigned((p.N + 63) / 64), unsigned((p.M + 63) / 64));
+    if (out == SGR_F32) int8_project_any_kernel<float><<<grid, 256, 0, s>>>(p);
+    else if (out == SGR_BF16) int8_project_any_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+    else int8_project_any_kernel<__half><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+sgr_status_t int8_quantize(const void *x, int64_t x_row_stride, int8_t *q, int64_t q_row_stride, float *scale,
+                           int64_t rows, int64_t K, sgr_dtype_t dtype, cudaStream_t stream) {
+    const int esz = host::float_size(dtype);
+    if (esz == 0 || rows < 0 || K < 0 || x_row_stride < 0 || q_row_stride < 0) return SGR_ERR_INVALID_ARG;
+    if (rows == 0) return SGR_OK;
+    if (!scale || (K > 0 && (!x || !q))) return SGR_ERR_INVALID_ARG;
+    if (rows > 1 && q_row_stride < K) return SGR_ERR_INVALID_ARG;
+    int64_t b_x, b_q, b_s;
+    if (!host::span_ok(rows, K, x_row_stride, esz, &b_x) || !host::span_ok(rows, K, q_row_stride, 1, &b_q) ||
+        !host::mul_ok(rows, 4, &b_s))
+        return SGR_ERR_UNSUPPORTED;
+    const Span out[2] = {{q, b_q}, {scale, b_s}}, in[1] = {{x, b_x}};
+    if (host::any_overlap(out, in)) return SGR_ERR_INVALID_ARG;
+    return quantize({x, x_row_stride, q, q_row_stride, scale, rows, K}, dtype, stream);
+}
+
+size_t sgr_int8_workspace_size(int64_t rows, int64_t K, sgr_dtype_t x_dtype) {
+    int64_t n = 0;
+    if (rows <= 0 || K <= 0 || K > kMaxK || host::float_size(x_dtype) == 0 || !host::mul_ok(rows, pad16(K) + 4, &n))
+        return 0;
+    return scale_at(rows, K) + size_t(rows) * 4;
+}
+
+sgr_status_t int8_projection(const void *x, int64_t x_row_stride, sgr_dtype_t x_dtype, const float *x_scale,
+                             const int8_t *w, int64_t w_row_stride, const float *w_scale, const float *bias, void *y,
+                             int64_t y_row_stride, sgr_dtype_t y_dtype, int64_t rows, int64_t K, int64_t N,
+                             void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    const int xsz = x_dtype == SGR_I8 ? 1 : host::float_size(x_dtype);
+    const int ysz = host::float_size(y_dtype);
+    if (xsz == 0 || ysz == 0 || rows < 0 || K < 0 || N < 0 || x_row_stride < 0 || w_row_stride < 0 || y_row_stride < 0)
+        return SGR_ERR_INVALID_ARG;
+    if (rows == 0 || N == 0) return SGR_OK;
+    if (K == 0 || !x || !w || !w_scale || !y || (x_dtype == SGR_I8) != (x_scale != nullptr)) return SGR_ERR_INVALID_ARG;
+    if (rows > 1 && y_row_stride < N) return SGR_ERR_INVALID_ARG;
+    if (K > kMaxK || rows > kMaxDim || N > kMaxDim) return SGR_ERR_UNSUPPORTED;
+    if ((rows + 63) / 64 > 65535) return SGR_ERR_UNSUPPORTED;
+    int64_t b_x, b_w, b_y, b_q;
+    if (!host::span_ok(rows, K, x_row_stride, xsz, &b_x) || !host::span_ok(N, K, w_row_stride, 1, &b_w) ||
+        !host::span_ok(rows, N, y_row_stride, ysz, &b_y) || !host::mul_ok(rows, pad16(K) + 4, &b_q))
+        return SGR_ERR_UNSUPPORTED;
+    const size_t need = sgr_int8_workspace_size(rows, K, x_dtype);
+    const Span out[2] = {{y, b_y}, {need ? workspace : nullptr, int64_t(need)}};
+    const Span in[5] = {{x, b_x}, {w, b_w}, {x_scale, rows * 4}, {w_scale, N * 4}, {bias, N * 4}};
+    if (host::any_overlap(out, in)) return SGR_ERR_INVALID_ARG;
+    if (need && (!workspace || ws_bytes < need || !host::aligned(workspace, 16))) return SGR_ERR_WORKSPACE;
+    ProjectParams p;
+    p.x = static_cast<const int8_t *>(x); p.x_rs = x_row_stride; p.x_scale = x_scale;
+    p.w = w; p.w_rs = w_row_stride; p.w_scale = w_scale; p.bias = bias;
+    p.y = y; p.y_rs = y_row_stride; p.M = rows; p.N = N; p.K = K;
+    if (x_dtype != SGR_I8) {
+        int8_t *q = static_cast<int8_t *>(workspace);
+        float *scale = reinterpret_cast<float *>(static_cast<char *>(workspace) + scale_at(rows, K));
+        const sgr_status_t st = quantize({x, x_row_stride, q, pad16(K), scale, rows, K}, x_dtype, stream);
+        if (st != SGR_OK) return st;
+        p.x = q; p.x_rs = pad16(K); p.x_scale = scale;
+    }
+    return product(p, y_dtype, stream);
+}
+
+}  // extern "C"

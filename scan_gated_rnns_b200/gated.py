@@ -1,0 +1,244 @@
+"""Torch-facing wrappers of the gated linear recurrence (argument marshalling
+only; every operation runs in ``libsgr.so``):
+
+    gated_scan(f, v, h0, cu_seqlens)     whole sequences, (B, T, D) or packed rows
+    gated_scan_backward(...)             its gradients
+    gated_scan_fn(f, v, h0, cu_seqlens)  the same, differentiable
+    gated_step(f, v, state, slots)       one token per request, states in a pool
+
+    gate="sigmoid":  a_t = sigmoid(f_t),      h_t = a_t h_{t-1} + (1 - a_t) v_t
+    gate="log":      a_t = exp(min(f_t, 0)),  h_t = a_t h_{t-1} + v_t
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _abi, ops
+from ._abi import check, lib
+
+_DT = {torch.float32: _abi.SGR_F32, torch.bfloat16: _abi.SGR_BF16, torch.float16: _abi.SGR_F16}
+_GATES = {"sigmoid": _abi.SGR_GATE_SIGMOID, "log": _abi.SGR_GATE_LOG}
+_INDEX = {torch.int32: 4, torch.int64: 8}
+
+
+def _gate(gate: str) -> int:
+    try:
+        return _GATES[gate]
+    except (KeyError, TypeError):
+        raise ValueError(f"gate must be 'sigmoid' or 'log', got {gate!r}") from None
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name}: dtype {t.dtype} is not supported (float32, bfloat16 or float16)") from None
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride, in elements, of a tensor whose leading dimensions count rows
+    that lie evenly spaced, each of them contiguous."""
+    shape, stride = t.shape, t.stride()
+    if shape[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    step, rows = None, 1
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != step * rows and t.numel():
+            raise ValueError(f"{name}: its leading dimensions must flatten to evenly spaced rows (make it contiguous)")
+        rows *= n
+    return shape[-1] if step is None else step
+
+
+def _operand(t: torch.Tensor, like: Optional[torch.Tensor], name: str) -> int:
+    ops._need_cuda(t, name)
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must match the first operand's shape, dtype and device")
+    return _row_stride(t, name)
+
+
+def _sequences(fn: str, f: torch.Tensor, cu: Optional[torch.Tensor]) -> Tuple[int, int, int, int, int]:
+    """(rows, D, sequences, pointer of the bounds, bytes of one)."""
+    if cu is None:
+        if f.dim() == 3:
+            return f.shape[0] * f.shape[1], f.shape[2], f.shape[0], 0, 0
+        if f.dim() == 2:
+            return f.shape[0], f.shape[1], 1, 0, 0
+        raise ValueError(f"{fn}: f must be (B, T, D) or (T, D), got shape {tuple(f.shape)}")
+    if f.dim() != 2:
+        raise ValueError(f"{fn}: with cu_seqlens f must be packed rows (N, D), got shape {tuple(f.shape)}")
+    ops._need_cuda(cu, fn + ": cu_seqlens")
+    if cu.dtype not in _INDEX or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous() or cu.device != f.device:
+        raise ValueError(f"{fn}: cu_seqlens must be a contiguous (sequences + 1,) int32 or int64 vector on {f.device}")
+    return f.shape[0], f.shape[1], cu.shape[0] - 1, cu.data_ptr(), _INDEX[cu.dtype]
+
+
+def _states(t: Optional[torch.Tensor], n: int, D: int, device, name: str, shared: bool) -> Tuple[int, int]:
+    """(pointer, row stride) of fp32 states (n, D), or (D,) where one may serve all."""
+    if t is None:
+        return 0, 0
+    ops._need_cuda(t, name)
+    if t.dtype != torch.float32 or t.device != device:
+        raise ValueError(f"{name} must be float32 on {device}")
+    if shared and t.dim() == 1:
+        if t.shape[0] != D or (D > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous (D,) vector")
+        return t.data_ptr(), 0
+    if tuple(t.shape) != (n, D) or (D > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be ({n}, {D}) with contiguous rows, got {tuple(t.shape)}")
+    return t.data_ptr(), (t.stride(0) if n > 1 else D)
+
+
+def _scratch(rows: int, D: int, device) -> Tuple[torch.Tensor, int]:
+    """The call's own workspace: of the caching allocator, so that calls on
+    other streams and captured graphs each have theirs."""
+    need = int(lib().sgr_gated_workspace_size(rows, D))
+    return torch.empty(max(need, 1), dtype=torch.uint8, device=device), need
+
+
+def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = None,
+               cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid",
+               out: Optional[torch.Tensor] = None, save_states: bool = False):
+    """(h, h_last): the gated linear recurrence over f, v, (B, T, D) or, with
+    cu_seqlens, packed rows (N, D); float32, bfloat16 or float16, rows of any
+    even spacing (the halves of one projection are read in place).
+
+    cu_seqlens: (S + 1,) ascending row bounds on the GPU; sequences may be
+    empty, and rows outside [cu[0], cu[-1]) are padding: 0 in the result, left
+    as they were in a given ``out``.  h0: float32 (S, D), or (D,) for every
+    sequence.  h_last: float32 (S, D), the state behind each sequence.  With
+    save_states a third result: what gated_scan_backward starts from."""
+    fn = "gated_scan"
+    g = _gate(gate)
+    f_rs = _operand(f, None, fn + ": f")
+    v_rs = _operand(v, f, fn + ": v")
+    dt = _dtype_code(f, fn)
+    rows, D, n, cp, cb = _sequences(fn, f, cu_seqlens)
+    hp, hss = _states(h0, n, D, f.device, fn + ": h0", True)
+    zero = out is None
+    if out is None:
+        out = torch.empty(f.shape, dtype=f.dtype, device=f.device)
+    o_rs = _operand(out, f, fn + ": out")
+    h_last = torch.empty((n, D), dtype=torch.float32, device=f.device)
+    chunks = int(lib().sgr_gated_chunks(rows))
+    states = torch.empty((chunks, D), dtype=torch.float32, device=f.device) if save_states else None
+    with torch.cuda.device(f.device):
+        ws, need = _scratch(rows, D, f.device)
+        code = lib().gated_scan(f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n, out.data_ptr(), o_rs,
+                                h_last.data_ptr(), states.data_ptr() if save_states else 0, rows, D, g, dt, int(zero),
+                                ws.data_ptr(), need, ops._stream(f.device))
+    check(fn, code)
+    return (out, h_last, states) if save_states else (out, h_last)
+
+
+def gated_scan_backward(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor], states: torch.Tensor,
+                        dh: torch.Tensor, dh_last: Optional[torch.Tensor] = None,
+                        cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid", want_dh0: bool = True):
+    """(df, dv, dh0) for dL/dh = dh and dL/dh_last = dh_last through
+    h, h_last, states = gated_scan(f, v, h0, cu_seqlens, gate, save_states=True);
+    dh0 is float32 (S, D), one row per sequence (None unless want_dh0)."""
+    fn = "gated_scan_backward"
+    g = _gate(gate)
+    f_rs = _operand(f, None, fn + ": f")
+    v_rs = _operand(v, f, fn + ": v")
+    dh_rs = _operand(dh, f, fn + ": dh")
+    dt = _dtype_code(f, fn)
+    rows, D, n, cp, cb = _sequences(fn, f, cu_seqlens)
+    hp, hss = _states(h0, n, D, f.device, fn + ": h0", True)
+    lp, lss = _states(dh_last, n, D, f.device, fn + ": dh_last", False)
+    if lp and n > 1 and lss != D:
+        raise ValueError(f"{fn}: dh_last must be contiguous")
+    chunks = int(lib().sgr_gated_chunks(rows))
+    sp, sss = _states(states, chunks, D, f.device, fn + ": states", False)
+    if states is None or (chunks > 1 and sss != D):
+        raise ValueError(f"{fn}: states must be the contiguous ({chunks}, {D}) tensor that gated_scan saved")
+    df = torch.empty(f.shape, dtype=f.dtype, device=f.device)
+    dv = torch.empty(f.shape, dtype=f.dtype, device=f.device)
+    dh0 = torch.empty((n, D), dtype=torch.float32, device=f.device) if want_dh0 else None
+    with torch.cuda.device(f.device):
+        ws, need = _scratch(rows, D, f.device)
+        code = lib().gated_scan_backward(f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n, sp, dh.data_ptr(),
+                                         dh_rs, lp, df.data_ptr(), D, dv.data_ptr(), D,
+                                         dh0.data_ptr() if want_dh0 else 0, rows, D, g, dt, ws.data_ptr(), need,
+                                         ops._stream(f.device))
+    check(fn, code)
+    return df, dv, dh0
+
+
+class GatedScan(torch.autograd.Function):
+    """The states that enter each chunk are kept for the backward pass (one
+    float32 row per 112 rows); the outputs are not."""
+
+    @staticmethod
+    def forward(ctx, f, v, h0, cu_seqlens, gate):
+        h, h_last, states = gated_scan(f, v, h0, cu_seqlens, gate, save_states=True)
+        ctx.save_for_backward(f, v, h0, cu_seqlens, states)
+        ctx.gate = gate
+        ctx.set_materialize_grads(False)
+        return h, h_last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dh_last):
+        f, v, h0, cu_seqlens, states = ctx.saved_tensors
+        if dh is None and dh_last is None:
+            return None, None, None, None, None
+        dh = torch.zeros_like(f) if dh is None else dh.contiguous()
+        df, dv, dh0 = gated_scan_backward(f, v, h0, states, dh, None if dh_last is None else dh_last.contiguous(),
+                                          cu_seqlens, ctx.gate, want_dh0=h0 is not None and ctx.needs_input_grad[2])
+        if dh0 is not None and h0.dim() == 1:
+            dh0 = dh0.sum(0)
+        return df, dv, dh0, None, None
+
+
+def gated_scan_fn(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = None,
+                  cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid"):
+    """(h, h_last) of gated_scan with gradients for f, v and h0, from either
+    result."""
+    return GatedScan.apply(f, v, h0, cu_seqlens, gate)
+
+
+def gated_step(f: torch.Tensor, v: torch.Tensor, state: torch.Tensor, slots: Optional[torch.Tensor] = None,
+               gate: str = "sigmoid", out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """h (M, D): one token of the recurrence for each of M requests; f, v (M, D)
+    rows, state the float32 pool (slots, D), updated in place.
+
+    slots: (M,) int32 or int64 on the GPU, the pool row of each request (None:
+    row i).  A slot outside the pool marks a padding row: 0 in the result, left
+    as it was in a given ``out``.  A slot named by several rows takes their
+    tokens in row order."""
+    fn = "gated_step"
+    g = _gate(gate)
+    f_rs = _operand(f, None, fn + ": f")
+    if f.dim() != 2:
+        raise ValueError(f"{fn}: f must be (M, D), got shape {tuple(f.shape)}")
+    v_rs = _operand(v, f, fn + ": v")
+    dt = _dtype_code(f, fn)
+    M, D = f.shape
+    if state.dim() != 2 or state.shape[1] != D:
+        raise ValueError(f"{fn}: state must be (slots, {D}), got {tuple(state.shape)}")
+    sp, srs = _states(state, state.shape[0], D, f.device, fn + ": state", False)
+    kp = kb = 0
+    if slots is not None:
+        ops._need_cuda(slots, fn + ": slots")
+        if slots.dtype not in _INDEX or tuple(slots.shape) != (M,) or not slots.is_contiguous() or \
+                slots.device != f.device:
+            raise ValueError(f"{fn}: slots must be a contiguous ({M},) int32 or int64 vector on {f.device}")
+        kp, kb = slots.data_ptr(), _INDEX[slots.dtype]
+    elif state.shape[0] < M:
+        raise ValueError(f"{fn}: state has {state.shape[0]} rows for {M} requests")
+    zero = out is None
+    if out is None:
+        out = torch.empty((M, D), dtype=f.dtype, device=f.device)
+    o_rs = _operand(out, f, fn + ": out")
+    with torch.cuda.device(f.device):
+        code = lib().gated_step(f.data_ptr(), f_rs, v.data_ptr(), v_rs, sp, srs, state.shape[0], kp, kb,
+                                out.data_ptr(), o_rs, M, D, g, dt, int(zero), ops._stream(f.device))
+    check(fn, code)
+    return out
