@@ -4,6 +4,8 @@
 
 #include "scan_gated_rnns.h"
 
+#include <cuda.h>
+
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
@@ -59,6 +61,25 @@ inline int sm_count(int dev) {
         cache[dev].store(v);
     }
     return v;
+}
+
+// cuTensorMapEncodeTiled, through the runtime; null if the driver lacks it
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiledFn encode_tiled() {
+    static std::atomic<EncodeTiledFn> fn{nullptr};
+    EncodeTiledFn f = fn.load();
+    if (f == nullptr) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || ptr == nullptr)
+            return nullptr;
+        f = reinterpret_cast<EncodeTiledFn>(ptr);
+        fn.store(f);
+    }
+    return f;
 }
 
 inline int float_size(sgr_dtype_t t) { return t == SGR_F32 ? 4 : (t == SGR_BF16 || t == SGR_F16 ? 2 : 0); }

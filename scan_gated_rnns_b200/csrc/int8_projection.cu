@@ -3,6 +3,7 @@
 // workspace and the launches.  No allocation, no synchronisation.
 #include "host_checks.h"
 #include "int8_projection.cuh"
+#include "int8_tensor.cuh"
 
 #include <algorithm>
 #include <limits>
@@ -30,7 +31,89 @@ sgr_status_t quantize(const QuantParams &p, sgr_dtype_t dtype, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
 }
 
+// Tensor map of 8-bit rows for boxes of 128 bytes x `box` rows, 128-byte
+// swizzle; bytes past the rows' ends read as zero.
+bool row_map(CUtensorMap *map, const int8_t *base, int64_t rows, int64_t K, int64_t rs, int box) {
+    const host::EncodeTiledFn enc = host::encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(rows > 1 ? rs : pad16(K))};
+    const cuuint32_t boxes[2] = {cuuint32_t(kKB), cuuint32_t(box)};
+    const cuuint32_t es[2] = {1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, boxes, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows that a tensor map can describe.
+bool mappable(const int8_t *base, int64_t rows, int64_t rs) {
+    return host::aligned(base, 16) && (rows <= 1 || (rs % 16 == 0 && rs > 0 && rs < (int64_t(1) << 40)));
+}
+
+template <int NT, typename OUT>
+cudaError_t launch_split(const ProjectParams &p, int sms, cudaStream_t s) {
+    using S = SplitShape<NT>;
+    const int64_t ct = (p.N + 127) / 128, tt = (p.M + NT - 1) / NT, n_kb = (p.K + kKB - 1) / kKB;
+    if (ct * tt > std::numeric_limits<int>::max() / 8) return cudaErrorInvalidConfiguration;
+    // as many parts of K as two blocks per SM take at once
+    int C = 1;
+    while (C < 8 && 2 * C <= n_kb && ct * tt * 2 * C <= 2 * sms) C *= 2;
+    CUtensorMap map_w, map_x;
+    if (!row_map(&map_w, p.w, p.N, p.K, p.w_rs, 128) || !row_map(&map_x, p.x, p.M, p.K, p.x_rs, NT))
+        return cudaErrorInvalidValue;
+    auto kernel = int8_project_split_kernel<NT, OUT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::smem_bytes));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(ct * tt * C));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = S::smem_bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, int(ct), C, map_w, map_x);
+}
+
+template <typename OUT>
+cudaError_t launch_pair(const ProjectParams &p, int sms, cudaStream_t s) {
+    const int64_t ct = (p.N + pair::kCh - 1) / pair::kCh, tt = (p.M + pair::kTok - 1) / pair::kTok;
+    if (ct * tt > std::numeric_limits<int>::max() / 2) return cudaErrorInvalidConfiguration;
+    CUtensorMap map_w, map_x;
+    if (!row_map(&map_w, p.w, p.N, p.K, p.w_rs, 128) || !row_map(&map_x, p.x, p.M, p.K, p.x_rs, 128))
+        return cudaErrorInvalidValue;
+    auto kernel = int8_project_pair_kernel<OUT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(pair::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    const unsigned grid = 2 * unsigned(std::min<int64_t>(ct * tt, sms / 2));
+    kernel<<<grid, pair::kThreads, pair::kSmemBytes, s>>>(p, int(ct), int(ct * tt), map_w, map_x);
+    return cudaGetLastError();
+}
+
+template <typename OUT>
+cudaError_t launch_tensor(const ProjectParams &p, int sms, cudaStream_t s) {
+    const int64_t pairs = ((p.N + 255) / 256) * ((p.M + 255) / 256);
+    if (p.M > 128 && 2 * pairs >= sms / 2) return launch_pair<OUT>(p, sms, s);
+    if (p.M <= 16) return launch_split<16, OUT>(p, sms, s);
+    if (p.M <= 32) return launch_split<32, OUT>(p, sms, s);
+    if (p.M <= 64) return launch_split<64, OUT>(p, sms, s);
+    return launch_split<128, OUT>(p, sms, s);
+}
+
 sgr_status_t product(const ProjectParams &p, sgr_dtype_t out, cudaStream_t s) {
+    if (mappable(p.w, p.N, p.w_rs) && mappable(p.x, p.M, p.x_rs)) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return SGR_ERR_CUDA;
+        const int sms = host::sm_count(dev);
+        if (sms <= 1) return SGR_ERR_CUDA;
+        const cudaError_t e = out == SGR_F32    ? launch_tensor<float>(p, sms, s)
+                              : out == SGR_BF16 ? launch_tensor<__nv_bfloat16>(p, sms, s)
+                                                : launch_tensor<__half>(p, sms, s);
+        return e == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
+    }
     const dim3 grid(unsigned((p.N + 63) / 64), unsigned((p.M + 63) / 64));
     if (out == SGR_F32) int8_project_any_kernel<float><<<grid, 256, 0, s>>>(p);
     else if (out == SGR_BF16) int8_project_any_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
