@@ -608,16 +608,17 @@ SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
  *   h          : (rows, D) in dtype.  h_last: fp32 (n_seqs, D), the state behind
  *                each sequence (h0 where it is empty), or NULL.
  *   states     : fp32 (sgr_gated_chunks(rows), D): the state entering every
- *                chunk of rows, what gated_scan_backward starts from (the row of
- *                a chunk that begins with a sequence is not written), or NULL.
+ *                chunk of rows, what gated_scan_backward starts from (unused, and
+ *                0, where the chunk begins with a sequence), or NULL.
  *   workspace  : sgr_gated_workspace_size(rows, D) bytes; need not be
  *                initialised and keeps nothing from call to call.  Not to be
  *                shared with another call that can run at the same time, nor
  *                with the entry points that keep hand-off words in theirs.
  * States and arithmetic are fp32.  A NaN or infinity stays within its sequence
  * and channel.  The result does not depend on how blocks are timed: equal
- * calls give equal bits.  Calls may be captured; a chunk that waited too long
- * leaves NaN and sets the workspace's status word.
+ * calls give equal bits.  Calls may be captured.  A chunk that waited too long
+ * leaves NaN and sets the workspace's first word to SGR_ERR_TIMEOUT (~0
+ * otherwise, behind a call that needs a workspace).
  */
 SGR_API sgr_status_t gated_scan(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride,
                                 const float *h0, int64_t h0_seq_stride, const void *cu_seqlens, int cu_bytes,

@@ -15,28 +15,27 @@ using namespace sgr;
 using namespace sgr::gated;
 using sgr::host::Span;
 
-constexpr size_t kHeader = 256;             // status word at 0, ticket at 64
+constexpr size_t kHeader = 256;             // status word at 0, ticket at 64 (its own sector)
 constexpr size_t kTicketAt = 64;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1 - kTR;
 constexpr int kBlocksPerSM = 2;
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Workspace: header, flags, maps, and the carried states (forward calls that
-// keep no states, and every backward call).
+// Workspace: header, then the words through which tiles hand their maps and
+// final states on.  Every byte is set to ~0 on the stream before the launch.
 struct Layout {
     int64_t n_strips, n_chunks, n_tiles;
-    size_t flags, maps, carry, total;
+    size_t maps, carry, total;
 };
 Layout layout(int64_t rows, int64_t D, int tc) {
     Layout l;
     l.n_strips = (D + tc - 1) / tc;
     l.n_chunks = (rows + kTR - 1) / kTR;
     l.n_tiles = l.n_strips * l.n_chunks;
-    l.flags = kHeader;
-    l.maps = align_up(l.flags + size_t(l.n_tiles) * 4, 256);
-    l.carry = align_up(l.maps + size_t(l.n_tiles) * tc * 8, 256);
-    l.total = align_up(l.carry + size_t(l.n_chunks) * size_t(D) * 4, 256);
+    l.maps = kHeader;
+    l.carry = l.maps + size_t(l.n_tiles) * tc * 8;
+    l.total = align_up(l.carry + size_t(l.n_tiles) * tc * 4, 256);
     return l;
 }
 
@@ -47,7 +46,25 @@ bool sizes_ok(int64_t rows, int64_t D) {
            ((rows + kTR - 1) / kTR) * ((D + 31) / 32) <= std::numeric_limits<int>::max();
 }
 
-template <typename IO, int E, int GATE>
+// Tensor map of (rows, D) for boxes of 128 bytes x kTR rows; what lies past
+// the edges reads as zero.
+bool tile_map(CUtensorMap *map, const void *base, int64_t rows, int64_t D, int64_t rs, int esz) {
+    const host::EncodeTiledFn enc = host::encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {rows > 1 ? cuuint64_t(rs) * esz : align_up(size_t(D) * esz, 16)};
+    const cuuint32_t box[2] = {cuuint32_t(128 / esz), cuuint32_t(kTR)};
+    const cuuint32_t es[2] = {1u, 1u};
+    return enc(map, esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+               const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool mappable(const void *base, int64_t rows, int64_t D, int64_t rs, int esz) {
+    return host::aligned(base, 16) && (rows <= 1 || (rs * esz % 16 == 0 && rs >= D && rs * esz < (int64_t(1) << 40)));
+}
+
+template <typename IO, int E, int GATE, bool TMA>
 cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -56,22 +73,48 @@ cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int64_t most = p.ticket ? int64_t(sms) * kBlocksPerSM : p.n_tiles;
     const unsigned grid = unsigned(std::max<int64_t>(1, std::min(p.n_tiles, most)));
-    if (backward) gated_scan_backward_kernel<IO, E, GATE><<<grid, kThreads, 0, s>>>(p);
-    else gated_scan_kernel<IO, E, GATE><<<grid, kThreads, 0, s>>>(p);
+    CUtensorMap m[3];
+    std::memset(m, 0, sizeof(m));
+    if (TMA) {
+        if (!tile_map(&m[0], p.f, p.rows, p.D, p.f_rs, sizeof(IO)) || !tile_map(&m[1], p.v, p.rows, p.D, p.v_rs, sizeof(IO)) ||
+            (backward && !tile_map(&m[2], p.dh, p.rows, p.D, p.dh_rs, sizeof(IO))))
+            return cudaErrorInvalidValue;
+    }
+    if (backward) {
+        constexpr uint32_t bytes = SmemShape<IO, E, 3, kBwdSlots, TMA>::bytes;
+        auto kernel = gated_scan_backward_kernel<IO, E, GATE, TMA>;
+        if (TMA && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
+            return e;
+        kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1], m[2]);
+    } else {
+        constexpr uint32_t bytes = SmemShape<IO, E, 2, kSlots, TMA>::bytes;
+        auto kernel = gated_scan_kernel<IO, E, GATE, TMA>;
+        if (TMA && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
+            return e;
+        kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1]);
+    }
     return cudaGetLastError();
 }
 
-template <typename IO, int E>
+template <typename IO, int E, bool TMA>
 cudaError_t launch_gate(const GatedParams &p, int gate, bool backward, cudaStream_t s) {
-    return gate == GATE_SIGMOID ? launch<IO, E, GATE_SIGMOID>(p, backward, s) : launch<IO, E, GATE_LOG>(p, backward, s);
+    return gate == GATE_SIGMOID ? launch<IO, E, GATE_SIGMOID, TMA>(p, backward, s)
+                                : launch<IO, E, GATE_LOG, TMA>(p, backward, s);
+}
+template <typename IO, int E>
+cudaError_t launch_e(const GatedParams &p, int gate, bool backward, bool tma, cudaStream_t s) {
+    return tma ? launch_gate<IO, E, true>(p, gate, backward, s) : launch_gate<IO, E, false>(p, gate, backward, s);
 }
 
 cudaError_t launch_any(const GatedParams &p, sgr_dtype_t dtype, int gate, int E, bool backward, cudaStream_t s) {
-    if (dtype == SGR_F32) return launch_gate<float, 1>(p, gate, backward, s);
+    const int esz = host::float_size(dtype);
+    const bool tma = p.rows > 0 && mappable(p.f, p.rows, p.D, p.f_rs, esz) && mappable(p.v, p.rows, p.D, p.v_rs, esz) &&
+                     (!backward || mappable(p.dh, p.rows, p.D, p.dh_rs, esz)) && (esz == 4 || E == 2);
+    if (dtype == SGR_F32) return launch_e<float, 1>(p, gate, backward, tma, s);
     if (dtype == SGR_BF16)
-        return E == 2 ? launch_gate<__nv_bfloat16, 2>(p, gate, backward, s)
-                      : launch_gate<__nv_bfloat16, 1>(p, gate, backward, s);
-    return E == 2 ? launch_gate<__half, 2>(p, gate, backward, s) : launch_gate<__half, 1>(p, gate, backward, s);
+        return E == 2 ? launch_e<__nv_bfloat16, 2>(p, gate, backward, tma, s)
+                      : launch_gate<__nv_bfloat16, 1, false>(p, gate, backward, s);
+    return E == 2 ? launch_e<__half, 2>(p, gate, backward, tma, s) : launch_gate<__half, 1, false>(p, gate, backward, s);
 }
 
 sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backward, void *ws, size_t ws_bytes,
@@ -135,12 +178,10 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
         char *w = static_cast<char *>(ws);
         p.status = reinterpret_cast<uint32_t *>(w);
         p.ticket = reinterpret_cast<uint32_t *>(w + kTicketAt);
-        p.flags = reinterpret_cast<uint32_t *>(w + l.flags);
-        p.maps = reinterpret_cast<float2 *>(w + l.maps);
-        p.carry = reinterpret_cast<float *>(w + l.carry);
-        if (!backward && !p.states) p.states = p.carry;
-        // nothing of an earlier call is read: status, ticket and flags are cleared on the stream
-        if (cudaMemsetAsync(w, 0, l.maps, stream) != cudaSuccess) return SGR_ERR_CUDA;
+        p.maps = reinterpret_cast<uint64_t *>(w + l.maps);
+        p.carry = reinterpret_cast<uint32_t *>(w + l.carry);
+        // nothing of an earlier call is read
+        if (cudaMemsetAsync(w, 0xff, l.carry + size_t(l.n_tiles) * 32 * E * 4, stream) != cudaSuccess) return SGR_ERR_CUDA;
     }
     return launch_any(p, dtype, gate == SGR_GATE_LOG ? GATE_LOG : GATE_SIGMOID, E, backward, stream) == cudaSuccess
                ? SGR_OK

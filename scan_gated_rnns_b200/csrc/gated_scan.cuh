@@ -15,13 +15,21 @@
 // and the carry warp finds the state that enters the tile; the threads then
 // replay their rows from it.  Inputs are read once and outputs written once.
 //
-// The carry between tiles of one channel strip: each publishes its map (flag
-// 1), finds the nearest earlier tile whose final state is published (flag 2),
-// applies the maps between, oldest first, and publishes its own final state.
-// The arithmetic is the sequential S_q = A_q S_{q-1} + B_q wherever that
-// state came from, so results do not depend on timing.  Blocks take tiles by
-// ticket in the order they run, so a wait is always for a tile that a running
-// block holds; waits are bounded.
+// The carry between tiles of one channel strip: each publishes its map, finds
+// the nearest earlier tile whose final state is published, applies the maps
+// between, oldest first, and publishes its own final state.  The arithmetic
+// is the sequential S_q = A_q S_{q-1} + B_q wherever that state came from, so
+// results do not depend on timing.  A map is one 64-bit word, a state one
+// 32-bit word per channel, all of them ~0 before the launch and valid once
+// they are not (arithmetic never gives that NaN), so a look-back is one round
+// trip to L2, without flags or fences.  Blocks take tiles by ticket in the
+// order they run, so a wait is always for a tile that a running block holds;
+// waits are bounded.
+//
+// Persistent blocks, two per SM.  The carry warp also keeps a ring of kSlots
+// tiles filled by the tensor memory accelerator (TMA; rows that start on
+// 16-byte boundaries; else the data warps load from memory themselves), and
+// hands each tile's table of sequence starts and ends over with it.
 #pragma once
 
 #include "gated_math.cuh"
@@ -33,7 +41,9 @@ constexpr int kWarps = 7;                  // data warps; the eighth carries
 constexpr int kRows = 16;                  // rows per data warp and thread
 constexpr int kTR = kWarps * kRows;        // rows per tile, and between saved states
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr uint32_t kFlagMap = 1, kFlagState = 2;
+constexpr int kSlots = 3;                  // forward ring
+constexpr int kBwdSlots = 2;               // backward ring
+constexpr uint32_t kNone = 0xffffffffu;    // a word not yet published
 
 struct GatedParams {
     const void *f, *v, *dh;                // (rows, D), unit stride along D
@@ -45,18 +55,17 @@ struct GatedParams {
     float *h_last;                         // (n_seqs, D) or null
     const float *dh_last;                  // (n_seqs, D) or null
     float *dh0;                            // (n_seqs, D) or null
-    float *states;                         // (n_chunks, D): forward: state entering each chunk
+    float *states;                         // (n_chunks, D): state entering each chunk, or null (forward)
     const void *cu;                        // n_seqs + 1 row bounds, or null: sequences of seq_rows rows
     int cu_bytes;                          // 4 or 8
     uint32_t seq_rows;
     int64_t rows, D, n_seqs;
     int64_t n_strips, n_chunks, n_tiles;
     int zero_padding;                      // outputs of rows in no sequence: 0 written, else left
-    float *carry;                          // backward: (n_chunks, D) as states, in processing order
-    float2 *maps;                          // [n_tiles][TC]
-    uint32_t *flags;                       // [n_strips][n_chunks], zero at launch
-    uint32_t *ticket;                      // zero at launch, or null: tile = blockIdx.x
-    uint32_t *status;                      // or null (one chunk: nothing waits)
+    uint64_t *maps;                        // [n_tiles][TC] words (A, B), ~0 at launch
+    uint32_t *carry;                       // [n_tiles][TC] words: state leaving each tile, ~0 at launch
+    uint32_t *ticket;                      // ~0 at launch, or null: tile = blockIdx.x
+    uint32_t *status;                      // ~0 at launch; SGR_ERR_TIMEOUT once a wait ran out; may be null
     uint32_t spin_limit;
 };
 
@@ -129,46 +138,44 @@ __device__ __forceinline__ void fill_info(const GatedParams &p, int64_t row0, Ti
     __syncwarp();
 }
 
-__device__ __forceinline__ uint32_t ld_acquire_u32(const uint32_t *p) {
+__device__ __forceinline__ uint32_t ld_relaxed_u32(const uint32_t *p) {
     uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_release_u32(uint32_t *p, uint32_t v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void st_relaxed_u32(uint32_t *p, uint32_t v) {
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-__device__ __forceinline__ float ld_relaxed_f32(const float *p) {
-    float v;
-    asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 ld_relaxed_f2(const float2 *p) {
-    const uint64_t v = ld_relaxed_u64(reinterpret_cast<const uint64_t *>(p));
-    return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+__device__ __forceinline__ uint64_t pack_map(float2 m) {
+    return (uint64_t(__float_as_uint(m.y)) << 32) | __float_as_uint(m.x);
 }
 
 // The carry of one tile (carry warp): q its place in processing order along
 // its strip, tot the tile's maps of this lane's E channels.  Publishes,
-// waits, and returns the entering states; `carry` row q + 1 receives the
-// final ones.  Tiles whose first row (in processing order) is a start enter
-// with 0, which they never use.
+// waits, and returns the entering states.  Tiles whose first row (in
+// processing order) is a start enter with 0, which they never use.  The
+// window holds the words of the W tiles before: all are read in one round
+// trip, and again only those not yet published.  W tiles are what one hop of
+// the chain advances (about 1 us); 16 (8 with two channels a lane) fit the
+// registers that the data warps' threads leave.
 template <int E>
-__device__ __forceinline__ void carry_tile_state(const GatedParams &p, float *carry, int64_t strip, int64_t q, int lane,
-                                                 bool fresh, const float2 (&tot)[E], float (&hin)[E]) {
+__device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int64_t q, int lane, bool fresh,
+                                                 const float2 (&tot)[E], float (&hin)[E]) {
     constexpr int TC = 32 * E;
-    const int64_t d0 = strip * TC + lane * E;
-    uint32_t *flags = p.flags + strip * p.n_chunks;
+    constexpr int W = E == 1 ? 16 : 8;
+    const int64_t step = p.n_strips * TC;                          // from a tile's words to the next chunk's
+    const int64_t at = q * step + strip * TC + lane * E;
     const bool last = q + 1 == p.n_chunks;
-    const bool cut = __any_sync(0xffffffffu, is_cut(tot[0].x));    // a start cuts all channels alike
+    bool cut = true;                                               // a start cuts all channels alike
 #pragma unroll
-    for (int e = 0; e < E; ++e) hin[e] = 0.f;
+    for (int e = 0; e < E; ++e) {
+        hin[e] = 0.f;
+        cut = cut && is_cut(tot[e].x);
+    }
     auto publish_state = [&] {
         if (last) return;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d0 + e < p.D) carry[(q + 1) * p.D + d0 + e] = apply_map(tot[e].x, tot[e].y, hin[e]);
-        __syncwarp();
-        if (lane == 0) st_release_u32(flags + q, kFlagState);
+        for (int e = 0; e < E; ++e) st_relaxed_u32(p.carry + at + e, __float_as_uint(apply_map(tot[e].x, tot[e].y, hin[e])));
     };
     if (fresh || q == 0) {
         publish_state();
@@ -178,52 +185,56 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, float *ca
         publish_state();
     } else if (!last) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) p.maps[(q * p.n_strips + strip) * TC + lane * E + e] = tot[e];
-        __syncwarp();
-        if (lane == 0) st_release_u32(flags + q, kFlagMap);
+        for (int e = 0; e < E; ++e) st_relaxed_u64(p.maps + at + e, pack_map(tot[e]));
     }
-    // the nearest published state among the 32 tiles before, all nearer maps there
-    int k = -1;
+    uint64_t m[W][E];
+    uint32_t st[W][E];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            m[i][e] = ~uint64_t(0);
+            st[i][e] = kNone;
+        }
+    }
+    int k = -1;                                                    // nearest published state, maps there before it
     for (uint32_t polls = 0;; ++polls) {
-        const int64_t i = q - 1 - lane;
-        const uint32_t fl = i >= 0 ? ld_acquire_u32(flags + i) : 0u;
-        const uint32_t state = __ballot_sync(0xffffffffu, fl == kFlagState);
-        const uint32_t any = __ballot_sync(0xffffffffu, fl != 0u);
-        if (state != 0u) {
-            k = __ffs(state) - 1;
-            const uint32_t nearer = (1u << k) - 1u;
-            if ((any & nearer) == nearer) break;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (q - 1 - i < 0) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (st[i][e] == kNone) st[i][e] = ld_relaxed_u32(p.carry + at + e - (i + 1) * step);
+                if (i < W - 1 && m[i][e] == ~uint64_t(0)) m[i][e] = ld_relaxed_u64(p.maps + at + e - (i + 1) * step);
+            }
         }
-        if (polls >= p.spin_limit) {
-            k = -1;
-            break;
+        bool there = true;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            bool s_ok = true, m_ok = true;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                s_ok = s_ok && st[i][e] != kNone;
+                m_ok = m_ok && m[i][e] != ~uint64_t(0);
+            }
+            if (there && k < 0 && s_ok) k = i;
+            there = there && m_ok;
         }
-        if (polls > 4) __nanosleep(64);
+        if (__all_sync(0xffffffffu, k >= 0) || polls >= p.spin_limit) break;
+        if (polls > 8) __nanosleep(32);
     }
-    __syncwarp();
     if (k < 0) {
-        if (lane == 0) atomicOr(p.status, kTimeoutBit);
+        atomicExch(p.status, 5u);                                  // SGR_ERR_TIMEOUT
 #pragma unroll
         for (int e = 0; e < E; ++e) hin[e] = __int_as_float(0x7fffffff);
     } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d0 + e < p.D) hin[e] = ld_relaxed_f32(carry + (q - k) * p.D + d0 + e);
-        for (int j = k; j > 0; j -= 4) {
-            float2 m[4][E];
+        for (int i = W - 1; i >= 0; --i) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    m[u][e] = j - u > 0 ? ld_relaxed_f2(p.maps + ((q - j + u) * p.n_strips + strip) * TC + lane * E + e)
-                                        : make_float2(1.f, 0.f);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (j - u > 0) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) hin[e] = apply_map(m[u][e].x, m[u][e].y, hin[e]);
-                }
+            for (int e = 0; e < E; ++e) {
+                if (i == k) hin[e] = __uint_as_float(st[i][e]);
+                else if (i < k)
+                    hin[e] = apply_map(__uint_as_float(uint32_t(m[i][e])), __uint_as_float(uint32_t(m[i][e] >> 32)), hin[e]);
             }
         }
     }
@@ -274,115 +285,259 @@ __device__ __forceinline__ void store_raw(void *base, int64_t off, typename Raw<
     __stcs(reinterpret_cast<typename Raw<IO, E>::type *>(static_cast<IO *>(base) + off), x);
 }
 
+
+// The tiles of a block, handed from the carry warp to the data warps through
+// a ring: tile n lies in slot n % S, its table in s_info[n % (S + 1)] (read
+// until the tile's replay is over, one tile longer than the slot).
+template <int S> struct Ring {
+    uint64_t full[S];
+    TileInfo info[S + 1];
+};
+
+template <typename IO, int E, int OPS, int S, bool TMA>
+struct SmemShape {
+    static constexpr int TC = 32 * E;
+    static constexpr uint32_t op_bytes = kTR * TC * sizeof(IO);
+    static constexpr uint32_t slot_bytes = OPS * op_bytes;
+    static constexpr uint32_t bytes = TMA ? S * slot_bytes + 128 : 0;
+};
+
+// The carry warp's side of the ring.  A tile is taken in three parts, so that
+// none of them delays the carry: next() draws its ticket, issue() starts its
+// copies as soon as the slot is free, finish() writes its table and lets the
+// data warps have it.  `reverse` counts chunks from the last.
+template <int S, int OPS, uint32_t OP_BYTES, int TC, bool TMA>
+struct Feed {
+    const GatedParams &p;
+    Ring<S> &ring;
+    const int lane;
+    const bool reverse;
+    const uint32_t slots;
+    const CUtensorMap *maps[3];
+    int64_t tile;                          // drawn, not yet finished; n_tiles: no more
+
+    __device__ __forceinline__ void next(bool first) {
+        if (p.ticket) {
+            if (!first && tile >= p.n_tiles) return;
+            uint32_t t = 0;
+            if (lane == 0) t = atomicAdd(p.ticket, 1u) + 1u;
+            tile = __shfl_sync(0xffffffffu, t, 0);
+        } else {
+            tile = first ? int64_t(blockIdx.x) : p.n_tiles;
+        }
+    }
+    __device__ __forceinline__ int64_t row0() const {
+        const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips);
+        return int64_t(reverse ? uint32_t(p.n_chunks) - 1 - q : q) * kTR;
+    }
+    __device__ __forceinline__ void issue(int n) {
+        if constexpr (TMA) {
+            if (lane == 0 && tile < p.n_tiles) {
+                const uint32_t strip = uint32_t(tile) % uint32_t(p.n_strips);
+                const uint32_t bar = smem_addr(&ring.full[n % S]);
+                const uint32_t dst = slots + uint32_t(n % S) * (OPS * OP_BYTES);
+                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(OPS * OP_BYTES)
+                             : "memory");
+#pragma unroll
+                for (int i = 0; i < OPS; ++i)
+                    tma_load_2d(dst + i * OP_BYTES, maps[i], int(strip) * TC, int(row0()), bar);
+            }
+            __syncwarp();
+        }
+    }
+    __device__ __forceinline__ void finish(int n) {
+        TileInfo &info = ring.info[n % (S + 1)];
+        if (tile < p.n_tiles) fill_info(p, row0(), info, lane);
+        if (lane == 0) info.tile = tile;
+        __syncwarp();
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&ring.full[n % S])) : "memory");
+    }
+};
+
+// Data warp: wait for tile n.  The table is always there in the end (the
+// carry warp's own waits are bounded); false means that copies are missing,
+// and the tile's outputs become NaN.
+__device__ __forceinline__ bool wait_tile(uint64_t *full, int n, int S, uint32_t &limit, uint32_t *status) {
+    if (mbar_wait(smem_addr(&full[n % S]), uint32_t((n / S) & 1), limit)) return true;
+    limit = 1;
+    if (status) atomicExch(status, 5u);                               // SGR_ERR_TIMEOUT
+    return false;
+}
+constexpr uint32_t kTileWait = 1u << 24;
+
+struct RowMasks {
+    uint32_t starts, ends, live;           // bit r: row r of the warp starts / ends a sequence, lies in one
+};
+__device__ __forceinline__ RowMasks row_masks(const TileInfo &info, int64_t row0, int warp, int lane) {
+    const int rr = lane & 15;
+    RowMasks k;
+    k.starts = __ballot_sync(0xffffffffu, info.start[warp * kRows + rr] >= 0) & 0xffffu;
+    k.ends = __ballot_sync(0xffffffffu, info.end[warp * kRows + rr] >= 0) & 0xffffu;
+    k.live = __ballot_sync(0xffffffffu, row0 + rr >= info.lo && row0 + rr < info.hi) & 0xffffu;
+    return k;
+}
+
+// The carry warp's part of a tile once the data warps' maps are in shared
+// memory: the entering state of each warp.  DIR +1: warps in order, -1: from
+// the last.
+template <int E, int DIR, class V>
+__device__ __forceinline__ void carry_warps(const GatedParams &p, const V (&sA)[kWarps][32], const V (&sB)[kWarps][32],
+                                            V (&sin)[kWarps][32], int64_t strip, int64_t q, int lane, bool fresh,
+                                            float *entering, int64_t d0) {
+    float2 pre[kWarps][E], tot[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) tot[e] = make_float2(1.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) {
+        const int w = DIR > 0 ? j : kWarps - 1 - j;
+        const float *A = reinterpret_cast<const float *>(&sA[w][lane]);
+        const float *B = reinterpret_cast<const float *>(&sB[w][lane]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            pre[j][e] = make_float2(A[e], B[e]);
+            tot[e] = then_map(tot[e], pre[j][e]);
+        }
+    }
+    float hin[E];
+    carry_tile_state<E>(p, strip, q, lane, fresh, tot, hin);
+    if (entering) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (d0 + e < p.D) entering[q * p.D + d0 + e] = hin[e];
+    }
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) {
+        const int w = DIR > 0 ? j : kWarps - 1 - j;
+        float *in = reinterpret_cast<float *>(&sin[w][lane]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            in[e] = hin[e];
+            hin[e] = apply_map(pre[j][e].x, pre[j][e].y, hin[e]);
+        }
+    }
+}
+
 // ------------------------------------------------------------- forward
-template <typename IO, int E, int GATE>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const GatedParams p) {
+template <typename IO, int E, int GATE, bool TMA>
+__global__ void __launch_bounds__(kThreads, 2)
+gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_v) {
     using V = typename FVec<E>::type;
     using R = typename Raw<IO, E>::type;
     using C = Conv<IO, E>;
+    using Shape = SmemShape<IO, E, 2, kSlots, TMA>;
     constexpr int TC = 32 * E;
-    __shared__ TileInfo s_info[2];
-    __shared__ V s_A[kWarps][32], s_B[kWarps][32], s_in[kWarps][32];
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Ring<kSlots> ring;
+    __shared__ V s_A[2][kWarps][32], s_B[2][kWarps][32], s_in[2][kWarps][32];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n_tiles = p.n_tiles;
-    auto prepare = [&](int par, bool first) {             // carry warp: the next tile and its table
-        int64_t tile = n_tiles;
-        if (p.ticket) {
-            uint32_t t = 0;
-            if (lane == 0) t = atomicAdd(p.ticket, 1u);
-            tile = __shfl_sync(0xffffffffu, t, 0);
-        } else if (first) {
-            tile = blockIdx.x;
-        }
-        if (tile < n_tiles) fill_info(p, int64_t(uint32_t(tile) / uint32_t(p.n_strips)) * kTR, s_info[par], lane);
-        if (lane == 0) s_info[par].tile = tile;
-        __syncwarp();
-    };
-    if (warp == kWarps) prepare(0, true);
-    for (int par = 0;; par ^= 1) {
-        __syncthreads();                                  // the table is there; the last tile's is free
-        const TileInfo &info = s_info[par];
-        const int64_t tile = info.tile;
-        if (tile >= n_tiles) break;
-        const int64_t chunk = uint32_t(tile) / uint32_t(p.n_strips), strip = tile - chunk * p.n_strips;
-        if (warp < kWarps) {
-            const int64_t row0 = chunk * kTR + warp * kRows;
-            const int64_t d0 = strip * TC + lane * E;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSlots; ++s) mbar_init(smem_addr(&ring.full[s]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (warp < kWarps) {
+        uint32_t limit = kTileWait;
+        for (int n = 0;; ++n) {
+            const int par = n & 1;
+            const bool got = wait_tile(ring.full, n, kSlots, limit, p.status);
+            const TileInfo &info = ring.info[n % (kSlots + 1)];
+            const int64_t tile = info.tile;
+            if (tile >= p.n_tiles) break;
+            const uint32_t chunk = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - chunk * uint32_t(p.n_strips);
+            const int64_t row0 = int64_t(chunk) * kTR + warp * kRows;
+            const int64_t d0 = int64_t(strip) * TC + lane * E;
             const bool dvalid = d0 < p.D;
+            const RowMasks k = row_masks(info, row0, warp, lane);
             R rf[kRows], rv[kRows];
+            if constexpr (TMA) {
+                const R *sf = reinterpret_cast<const R *>(smem + (n % kSlots) * Shape::slot_bytes) + warp * kRows * 32 + lane;
+                const R *sv = sf + kTR * 32;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const bool ok = dvalid && row0 + r < p.rows;
-                rf[r] = ok ? load_raw<IO, E>(p.f, (row0 + r) * p.f_rs + d0) : R(0);
-                rv[r] = ok ? load_raw<IO, E>(p.v, (row0 + r) * p.v_rs + d0) : R(0);
+                for (int r = 0; r < kRows; ++r) {
+                    rf[r] = sf[r * 32];
+                    rv[r] = sv[r * 32];
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const bool ok = dvalid && row0 + r < p.rows;
+                    rf[r] = ok ? load_raw<IO, E>(p.f, (row0 + r) * p.f_rs + d0) : R(0);
+                    rv[r] = ok ? load_raw<IO, E>(p.v, (row0 + r) * p.v_rs + d0) : R(0);
+                }
             }
-            // rows of this warp that start or end a sequence, and that lie in one
-            const int rr = lane & 15;
-            const uint32_t starts = __ballot_sync(0xffffffffu, info.start[warp * kRows + rr] >= 0) & 0xffffu;
-            const uint32_t ends = __ballot_sync(0xffffffffu, info.end[warp * kRows + rr] >= 0) & 0xffffu;
-            const uint32_t live =
-                __ballot_sync(0xffffffffu, row0 + rr >= info.lo && row0 + rr < info.hi) & 0xffffu;
             V a[kRows], b[kRows];
             V A = vset<V>(1.f), B = vset<V>(0.f);
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a[r], b[r]);
-                if (starts >> r & 1u) {
+                if (k.starts >> r & 1u) {
                     A = vset<V>(-0.f);
                     B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
                 }
                 B = vfma(a[r], B, b[r]);
                 A = vmul(A, a[r]);
             }
-            s_A[warp][lane] = A;
-            s_B[warp][lane] = B;
-            named_barrier_arrive(1, kThreads);
-            named_barrier_sync(2, kThreads);
-            V h = s_in[warp][lane];
+            if (!got) {
+                A = B = vset<V>(__int_as_float(0x7fffffff));
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
-                h = vfma(a[r], h, b[r]);
-                if (live >> r & 1u) {
-                    if (dvalid) store_raw<IO, E>(p.h, (row0 + r) * p.h_rs + d0, C::out(h));
-                } else if (p.zero_padding && dvalid && row0 + r < p.rows) {
-                    store_raw<IO, E>(p.h, (row0 + r) * p.h_rs + d0, R(0));
+                for (int r = 0; r < kRows; ++r) b[r] = B;
+            }
+            s_A[par][warp][lane] = A;
+            s_B[par][warp][lane] = B;
+            named_barrier_arrive(1 + par, kThreads);
+            named_barrier_sync(3 + par, kThreads);
+            V h = s_in[par][warp][lane];
+            char *dst = static_cast<char *>(p.h) + (row0 * p.h_rs + d0) * int64_t(sizeof(IO));
+            const int64_t pitch = p.h_rs * int64_t(sizeof(IO));
+            if (k.starts == 0u && k.ends == 0u && k.live == 0xffffu) {
+                if (dvalid) {
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        h = vfma(a[r], h, b[r]);
+                        __stcs(reinterpret_cast<R *>(dst), C::out(h));
+                        dst += pitch;
+                    }
                 }
-                if (ends >> r & 1u) {
-                    if (p.h_last) put_state_row<E>(p.h_last, info.end[warp * kRows + r] * p.D, d0, p.D, h);
+            } else {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    if (k.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
+                    h = vfma(a[r], h, b[r]);
+                    if (dvalid && row0 + r < p.rows) {
+                        if (k.live >> r & 1u) __stcs(reinterpret_cast<R *>(dst), C::out(h));
+                        else if (p.zero_padding) __stcs(reinterpret_cast<R *>(dst), R(0));
+                    }
+                    dst += pitch;
+                    if ((k.ends >> r & 1u) && p.h_last) put_state_row<E>(p.h_last, info.end[warp * kRows + r] * p.D, d0, p.D, h);
                 }
             }
-        } else {
-            prepare(par ^ 1, false);
-            named_barrier_sync(1, kThreads);
-            float2 pre[kWarps][E], tot[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) tot[e] = make_float2(1.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float *A = reinterpret_cast<const float *>(&s_A[w][lane]);
-                const float *B = reinterpret_cast<const float *>(&s_B[w][lane]);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    pre[w][e] = make_float2(A[e], B[e]);
-                    tot[e] = then_map(tot[e], pre[w][e]);
-                }
-            }
-            float hin[E];
-            carry_tile_state<E>(p, p.states, strip, chunk, lane, info.start[0] >= 0, tot, hin);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                float *in = reinterpret_cast<float *>(&s_in[w][lane]);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    in[e] = hin[e];
-                    hin[e] = apply_map(pre[w][e].x, pre[w][e].y, hin[e]);
-                }
-            }
-            named_barrier_arrive(2, kThreads);
+        }
+    } else {
+        Feed<kSlots, 2, Shape::op_bytes, TC, TMA> feed{p, ring, lane, false, smem_addr(smem), {&map_f, &map_v, nullptr}, 0};
+        for (int n = 0; n < kSlots; ++n) {
+            feed.next(n == 0);
+            feed.issue(n);
+            feed.finish(n);
+        }
+        feed.next(false);
+        for (int n = 0;; ++n) {
+            const int par = n & 1;
+            const TileInfo &info = ring.info[n % (kSlots + 1)];
+            const int64_t tile = info.tile;
+            if (tile >= p.n_tiles) break;
+            const uint32_t chunk = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - chunk * uint32_t(p.n_strips);
+            const bool fresh = info.start[0] >= 0;
+            named_barrier_sync(1 + par, kThreads);         // the maps are there, and the slot has been read
+            feed.issue(n + kSlots);
+            carry_warps<E, 1>(p, s_A[par], s_B[par], s_in[par], strip, chunk, lane, fresh, p.states,
+                              int64_t(strip) * TC + lane * E);
+            named_barrier_arrive(3 + par, kThreads);
+            feed.finish(n + kSlots);
+            feed.next(false);
         }
     }
+    __syncthreads();
     empty_sequences(p, p.h_last, p.h0, p.h0_ss);
 }
 
@@ -398,79 +553,103 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const GatedPara
 // D per kTR rows), instead of being read back: the outputs h are not needed,
 // so the pass reads three arrays and not four, and the states have not been
 // rounded to 16 bits.
-template <typename IO, int E, int GATE>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const GatedParams p) {
+//
+// The tile's slot is read three times (folds, forward replay, reverse
+// replay), so it is refilled once the next tile's maps are in; the registers
+// hold the gates and the factors of df.
+template <int GATE, typename IO, class V>
+__device__ __forceinline__ V bwd_gate(V f) {
+    // GATE_SIGMOID: signed small probability; GATE_LOG: a, negated where f > 0, which has no gradient
+    if constexpr (GATE == GATE_SIGMOID) return vmap(f, [](float x) { return signed_small(x); });
+    else
+        return vmap(f, [](float x) {
+            const float t = log_decay<sizeof(IO) == 4>(x);
+            return x > 0.f ? -t : t;
+        });
+}
+template <int GATE, class V>
+__device__ __forceinline__ V bwd_a(V s) {
+    if constexpr (GATE == GATE_SIGMOID) {
+        V a, z;
+        split_small(s, a, z);
+        return a;
+    } else {
+        return vmap(s, [](float x) { return fabsf(x); });
+    }
+}
+
+template <typename IO, int E, int GATE, bool TMA>
+__global__ void __launch_bounds__(kThreads, 2)
+gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f,
+                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dh) {
     using V = typename FVec<E>::type;
     using R = typename Raw<IO, E>::type;
     using C = Conv<IO, E>;
+    using Shape = SmemShape<IO, E, 3, kBwdSlots, TMA>;
     constexpr int TC = 32 * E;
-    __shared__ TileInfo s_info[2];
-    __shared__ V s_A[kWarps][32], s_B[kWarps][32];        // forward maps
-    __shared__ V s_RA[kWarps][32], s_RB[kWarps][32];      // reverse maps
-    __shared__ V s_in[kWarps][32];
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Ring<kBwdSlots> ring;
+    __shared__ V s_A[kWarps][32], s_B[kWarps][32];                    // forward maps
+    __shared__ V s_RA[2][kWarps][32], s_RB[2][kWarps][32];            // reverse maps
+    __shared__ V s_in[2][kWarps][32];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n_tiles = p.n_tiles;
-    auto prepare = [&](int par, bool first) {
-        int64_t tile = n_tiles;
-        if (p.ticket) {
-            uint32_t t = 0;
-            if (lane == 0) t = atomicAdd(p.ticket, 1u);
-            tile = __shfl_sync(0xffffffffu, t, 0);
-        } else if (first) {
-            tile = blockIdx.x;
-        }
-        if (tile < n_tiles) fill_info(p, (p.n_chunks - 1 - uint32_t(tile) / uint32_t(p.n_strips)) * kTR, s_info[par], lane);
-        if (lane == 0) s_info[par].tile = tile;
-        __syncwarp();
-    };
-    if (warp == kWarps) prepare(0, true);
-    for (int par = 0;; par ^= 1) {
-        __syncthreads();
-        const TileInfo &info = s_info[par];
-        const int64_t tile = info.tile;
-        if (tile >= n_tiles) break;
-        const int64_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = tile - q * p.n_strips, chunk = p.n_chunks - 1 - q;
-        if (warp < kWarps) {
-            const int64_t row0 = chunk * kTR + warp * kRows;
-            const int64_t d0 = strip * TC + lane * E;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kBwdSlots; ++s) mbar_init(smem_addr(&ring.full[s]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (warp < kWarps) {
+        uint32_t limit = kTileWait;
+        for (int n = 0;; ++n) {
+            const int par = n & 1;
+            const bool got = wait_tile(ring.full, n, kBwdSlots, limit, p.status);
+            const TileInfo &info = ring.info[n % (kBwdSlots + 1)];
+            const int64_t tile = info.tile;
+            if (tile >= p.n_tiles) break;
+            const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
+            const uint32_t chunk = uint32_t(p.n_chunks) - 1 - q;
+            const int64_t row0 = int64_t(chunk) * kTR + warp * kRows;
+            const int64_t d0 = int64_t(strip) * TC + lane * E;
             const bool dvalid = d0 < p.D;
-            R rf[kRows], rv[kRows], rg[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const bool ok = dvalid && row0 + r < p.rows;
-                rf[r] = ok ? load_raw<IO, E>(p.f, (row0 + r) * p.f_rs + d0) : R(0);
-                rv[r] = ok ? load_raw<IO, E>(p.v, (row0 + r) * p.v_rs + d0) : R(0);
-                rg[r] = ok ? load_raw<IO, E>(p.dh, (row0 + r) * p.dh_rs + d0) : R(0);
-            }
             V h = info.start[0] >= 0 || chunk == 0 ? vset<V>(0.f) : state_row<E>(p.states, chunk * p.D, d0, p.D);
-            const int rr = lane & 15;
-            const uint32_t starts = __ballot_sync(0xffffffffu, info.start[warp * kRows + rr] >= 0) & 0xffffu;
-            const uint32_t ends = __ballot_sync(0xffffffffu, info.end[warp * kRows + rr] >= 0) & 0xffffu;
-            const uint32_t live =
-                __ballot_sync(0xffffffffu, row0 + rr >= info.lo && row0 + rr < info.hi) & 0xffffu;
-            // s: the gate of each row (GATE_SIGMOID: signed small probability; GATE_LOG: a,
-            // negated where f > 0, which has no gradient)
+            const RowMasks k = row_masks(info, row0, warp, lane);
+            [[maybe_unused]] R gv[TMA ? 1 : kRows], gg[TMA ? 1 : kRows];
+            const R *sf = reinterpret_cast<const R *>(smem + (n % kBwdSlots) * Shape::slot_bytes) + warp * kRows * 32 + lane;
+            if constexpr (!TMA) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const bool ok = dvalid && row0 + r < p.rows;
+                    gv[r] = ok ? load_raw<IO, E>(p.v, (row0 + r) * p.v_rs + d0) : R(0);
+                    gg[r] = ok ? load_raw<IO, E>(p.dh, (row0 + r) * p.dh_rs + d0) : R(0);
+                }
+            }
+            auto in_f = [&](int r) {
+                if constexpr (TMA) return C::in(sf[r * 32]);
+                else return C::in(dvalid && row0 + r < p.rows ? load_raw<IO, E>(p.f, (row0 + r) * p.f_rs + d0) : R(0));
+            };
+            auto in_v = [&](int r) {
+                if constexpr (TMA) return C::in(sf[(kTR + r) * 32]);
+                else return C::in(gv[r]);
+            };
+            auto in_g = [&](int r) {
+                if constexpr (TMA) return C::in(sf[(2 * kTR + r) * 32]);
+                else return C::in(gg[r]);
+            };
             V s[kRows];
             V A = vset<V>(1.f), B = vset<V>(0.f);
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                V a, b;
-                const V f = C::in(rf[r]), v = C::in(rv[r]);
+                s[r] = bwd_gate<GATE, IO>(in_f(r));
+                V a, b = in_v(r);
                 if constexpr (GATE == GATE_SIGMOID) {
                     V z;
-                    s[r] = vmap(f, [](float x) { return signed_small(x); });
                     split_small(s[r], a, z);
-                    b = vmul(z, v);
+                    b = vmul(z, b);
                 } else {
-                    s[r] = vmap(f, [](float x) {
-                        const float t = log_decay<sizeof(IO) == 4>(x);
-                        return x > 0.f ? -t : t;
-                    });
-                    a = vmap(s[r], [](float x) { return fabsf(x); });
-                    b = v;
+                    a = bwd_a<GATE>(s[r]);
                 }
-                if (starts >> r & 1u) {
+                if (k.starts >> r & 1u) {
                     A = vset<V>(-0.f);
                     B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
                 }
@@ -480,100 +659,91 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
             V RA = vset<V>(1.f), RB = vset<V>(0.f);
 #pragma unroll
             for (int r = kRows - 1; r >= 0; --r) {
-                V a, z;
-                if constexpr (GATE == GATE_SIGMOID) split_small(s[r], a, z);
-                else a = vmap(s[r], [](float x) { return fabsf(x); });
-                if (ends >> r & 1u) {
+                const V a = bwd_a<GATE>(s[r]);
+                if (k.ends >> r & 1u) {
                     RA = vset<V>(-0.f);
                     RB = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, d0, p.D);
                 }
-                RB = vmul(a, vadd(RB, C::in(rg[r])));
+                RB = vmul(a, vadd(RB, in_g(r)));
                 RA = vmul(RA, a);
+            }
+            if (!got) {
+                A = B = RA = RB = vset<V>(__int_as_float(0x7fffffff));
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) s[r] = B;
             }
             s_A[warp][lane] = A;
             s_B[warp][lane] = B;
-            s_RA[warp][lane] = RA;
-            s_RB[warp][lane] = RB;
-            named_barrier_arrive(1, kThreads);
-            named_barrier_sync(3, kWarps * 32);           // the data warps' maps are there
-            for (int w = 0; w < warp; ++w) {
-                const V a = s_A[w][lane], b = s_B[w][lane];
-                h = vmap(a, b, h, [](float x, float y, float z) { return apply_map(x, y, z); });
-            }
-            V c[kRows];                                   // df = c g
+            s_RA[par][warp][lane] = RA;
+            s_RB[par][warp][lane] = RB;
+            named_barrier_arrive(1 + par, kThreads);
+            named_barrier_sync(5, kWarps * 32);                       // the data warps' maps are there
+            for (int w = 0; w < warp; ++w)
+                h = vmap(s_A[w][lane], s_B[w][lane], h, [](float x, float y, float z) { return apply_map(x, y, z); });
+            V c[kRows];                                               // df = c g
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                if (starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
-                const V v = C::in(rv[r]);
+                if (k.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
+                const V v = in_v(r);
                 if constexpr (GATE == GATE_SIGMOID) {
                     V a, z;
                     split_small(s[r], a, z);
-                    c[r] = vmul(vmul(a, z), vadd(h, vmul(v, vset<V>(-1.f))));
+                    c[r] = vmul(vmul(a, z), vfma(v, vset<V>(-1.f), h));
                     h = vfma(a, h, vmul(z, v));
                 } else {
                     c[r] = vmap(s[r], h, [](float x, float y) { return is_cut(x) ? 0.f : x * y; });
-                    h = vfma(vmap(s[r], [](float x) { return fabsf(x); }), h, v);
+                    h = vfma(bwd_a<GATE>(s[r]), h, v);
                 }
             }
-            named_barrier_sync(2, kThreads);
-            V flow = s_in[warp][lane];
+            named_barrier_sync(3 + par, kThreads);
+            V flow = s_in[par][warp][lane];
 #pragma unroll
             for (int r = kRows - 1; r >= 0; --r) {
-                if (ends >> r & 1u) flow = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, d0, p.D);
-                const V g = vadd(flow, C::in(rg[r]));
-                V a, gv;
+                if (k.ends >> r & 1u) flow = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, d0, p.D);
+                const V g = vadd(flow, in_g(r));
+                V a, dv = g;
                 if constexpr (GATE == GATE_SIGMOID) {
                     V z;
                     split_small(s[r], a, z);
-                    gv = vmul(z, g);
+                    dv = vmul(z, g);
                 } else {
-                    a = vmap(s[r], [](float x) { return fabsf(x); });
-                    gv = g;
+                    a = bwd_a<GATE>(s[r]);
                 }
                 if (dvalid && row0 + r < p.rows) {
-                    if (live >> r & 1u) {
-                        store_raw<IO, E>(p.df, (row0 + r) * p.df_rs + d0, C::out(vmul(c[r], g)));
-                        store_raw<IO, E>(p.dv, (row0 + r) * p.dv_rs + d0, C::out(gv));
-                    } else {
-                        store_raw<IO, E>(p.df, (row0 + r) * p.df_rs + d0, R(0));
-                        store_raw<IO, E>(p.dv, (row0 + r) * p.dv_rs + d0, R(0));
-                    }
+                    const bool live = k.live >> r & 1u;
+                    store_raw<IO, E>(p.df, (row0 + r) * p.df_rs + d0, live ? C::out(vmul(c[r], g)) : R(0));
+                    store_raw<IO, E>(p.dv, (row0 + r) * p.dv_rs + d0, live ? C::out(dv) : R(0));
                 }
                 flow = vmul(a, g);
-                if (starts >> r & 1u) {
-                    if (p.dh0) put_state_row<E>(p.dh0, info.start[warp * kRows + r] * p.D, d0, p.D, flow);
-                }
+                if ((k.starts >> r & 1u) && p.dh0) put_state_row<E>(p.dh0, info.start[warp * kRows + r] * p.D, d0, p.D, flow);
             }
-        } else {
-            prepare(par ^ 1, false);
-            named_barrier_sync(1, kThreads);
-            float2 pre[kWarps][E], tot[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) tot[e] = make_float2(1.f, 0.f);
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                const float *A = reinterpret_cast<const float *>(&s_RA[w][lane]);
-                const float *B = reinterpret_cast<const float *>(&s_RB[w][lane]);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    pre[w][e] = make_float2(A[e], B[e]);
-                    tot[e] = then_map(tot[e], pre[w][e]);
-                }
+        }
+    } else {
+        Feed<kBwdSlots, 3, Shape::op_bytes, TC, TMA> feed{p, ring, lane, true, smem_addr(smem), {&map_f, &map_v, &map_dh}, 0};
+        for (int n = 0; n < kBwdSlots; ++n) {
+            feed.next(n == 0);
+            feed.issue(n);
+            feed.finish(n);
+        }
+        feed.next(false);
+        for (int n = 0;; ++n) {
+            const int par = n & 1;
+            const TileInfo &info = ring.info[n % (kBwdSlots + 1)];
+            const int64_t tile = info.tile;
+            if (tile >= p.n_tiles) break;
+            const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
+            const bool fresh = info.end[kTR - 1] >= 0;
+            named_barrier_sync(1 + par, kThreads);         // every data warp has left tile n - 1 behind
+            if (n >= 1) feed.issue(n + kBwdSlots - 1);     // ... whose slot takes this one
+            carry_warps<E, -1>(p, s_RA[par], s_RB[par], s_in[par], strip, q, lane, fresh, nullptr, 0);
+            named_barrier_arrive(3 + par, kThreads);
+            if (n >= 1) {
+                feed.finish(n + kBwdSlots - 1);
+                feed.next(false);
             }
-            float hin[E];
-            carry_tile_state<E>(p, p.carry, strip, q, lane, info.end[kTR - 1] >= 0, tot, hin);
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                float *in = reinterpret_cast<float *>(&s_in[w][lane]);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    in[e] = hin[e];
-                    hin[e] = apply_map(pre[w][e].x, pre[w][e].y, hin[e]);
-                }
-            }
-            named_barrier_arrive(2, kThreads);
         }
     }
+    __syncthreads();
     empty_sequences(p, p.dh0, p.dh_last, p.D);
 }
 
