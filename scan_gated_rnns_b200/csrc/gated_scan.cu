@@ -18,7 +18,6 @@ using sgr::host::Span;
 constexpr size_t kHeader = 256;             // status word at 0, ticket at 64 (its own sector)
 constexpr size_t kTicketAt = 64;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1 - kTR;
-constexpr int kBlocksPerSM = 2;
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -71,7 +70,7 @@ cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int sms = host::sm_count(dev);
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int64_t most = p.ticket ? int64_t(sms) * kBlocksPerSM : p.n_tiles;
+    const int64_t most = p.ticket ? int64_t(sms) : p.n_tiles;
     const unsigned grid = unsigned(std::max<int64_t>(1, std::min(p.n_tiles, most)));
     CUtensorMap m[3];
     std::memset(m, 0, sizeof(m));
@@ -81,15 +80,17 @@ cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
             return cudaErrorInvalidValue;
     }
     if (backward) {
-        constexpr uint32_t bytes = SmemShape<IO, E, 3, kBwdSlots, TMA>::bytes;
+        constexpr uint32_t bytes = BackwardShape<IO, E, TMA>::smem_bytes;
         auto kernel = gated_scan_backward_kernel<IO, E, GATE, TMA>;
-        if (TMA && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
+        static_assert(bytes <= 227 * 1024, "one block per SM");
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
             return e;
         kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1], m[2]);
     } else {
-        constexpr uint32_t bytes = SmemShape<IO, E, 2, kSlots, TMA>::bytes;
+        constexpr uint32_t bytes = ForwardShape<IO, E, TMA>::smem_bytes;
         auto kernel = gated_scan_kernel<IO, E, GATE, TMA>;
-        if (TMA && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
+        static_assert(bytes <= 227 * 1024, "one block per SM");
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
             return e;
         kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1]);
     }

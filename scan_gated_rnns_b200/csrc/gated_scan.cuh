@@ -10,10 +10,10 @@
 // earlier sequence held (infinities, NaN) reaches a later one.
 //
 // A tile is kTR rows x TC channels (128 bytes of a row).  Data warp w owns
-// rows [16 w, 16 w + 16), lane l channels [E l, E l + E): a thread folds its
-// 16 rows in registers, the seven folds of a channel meet in shared memory,
-// and the carry warp finds the state that enters the tile; the threads then
-// replay their rows from it.  Inputs are read once and outputs written once.
+// rows [8 w, 8 w + 8), lane l channels [E l, E l + E): a thread folds its 8
+// rows, the folds of a channel meet in shared memory, and a carry warp finds
+// the state that enters the tile; the threads then replay their rows from it.
+// Inputs are read from memory once and outputs written once.
 //
 // The carry between tiles of one channel strip: each publishes its map, finds
 // the nearest earlier tile whose final state is published, applies the maps
@@ -26,10 +26,15 @@
 // order they run, so a wait is always for a tile that a running block holds;
 // waits are bounded.
 //
-// Persistent blocks, two per SM.  The carry warp also keeps a ring of kSlots
-// tiles filled by the tensor memory accelerator (TMA; rows that start on
-// 16-byte boundaries; else the data warps load from memory themselves), and
-// hands each tile's table of sequence starts and ends over with it.
+// One persistent block per SM.  The feeding warp keeps a ring of tiles in
+// shared memory filled by the tensor memory accelerator (TMA; rows that start
+// on 16-byte boundaries, else the data warps load from memory themselves) and
+// writes each tile's table of sequence starts and ends.  A tile's state takes
+// two or three microseconds to arrive, longer than its arithmetic, so the
+// data warps fold tile n and then replay tile n - kLag, evaluating its gates
+// again from the ring: the second evaluation costs less than holding two
+// values per element in registers across the wait, which left room for two
+// tiles per SM only (bf16 32768 x 4096, sigmoid: 307 us that way).
 #pragma once
 
 #include "gated_math.cuh"
@@ -37,12 +42,14 @@
 namespace sgr {
 namespace gated {
 
-constexpr int kWarps = 7;                  // data warps; the eighth carries
-constexpr int kRows = 16;                  // rows per data warp and thread
+constexpr int kWarps = 13;                 // data warps
+constexpr int kRows = 8;                   // rows per data warp and thread
 constexpr int kTR = kWarps * kRows;        // rows per tile, and between saved states
-constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kSlots = 3;                  // forward ring
-constexpr int kBwdSlots = 2;               // backward ring
+constexpr int kCarryWarps = 2;             // tiles in turn
+constexpr int kThreads = (kWarps + kCarryWarps + 1) * 32;   // the last warp feeds the ring
+constexpr int kSlots = 6, kLag = 2;        // forward: tiles in shared memory, tiles between fold and replay
+constexpr int kBwdSlots = 4, kBwdLag = 1;  // backward
+constexpr uint32_t kTileWait = 1u << 16;   // polls of a wait inside the block (each suspends for tens of us)
 constexpr uint32_t kNone = 0xffffffffu;    // a word not yet published
 
 struct GatedParams {
@@ -77,7 +84,7 @@ __device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) >> 3
 // the map (A, B) applied to a state, and `then` after `first`
 __device__ __forceinline__ float apply_map(float A, float B, float h) { return is_cut(A) ? B : fmaf(A, h, B); }
 __device__ __forceinline__ float2 then_map(float2 first, float2 then) {
-    return make_float2(first.x * then.x, is_cut(then.x) ? then.y : fmaf(then.x, first.y, then.y));
+    return is_cut(then.x) ? then : make_float2(first.x * then.x, fmaf(then.x, first.y, then.y));
 }
 
 // What the carry warp tells the data warps of a tile.
@@ -157,10 +164,11 @@ __device__ __forceinline__ uint64_t pack_map(float2 m) {
 // window holds the words of the W tiles before: all are read in one round
 // trip, and again only those not yet published.  W tiles are what one hop of
 // the chain advances (about 1 us); 16 (8 with two channels a lane) fit the
-// registers that the data warps' threads leave.
-template <int E>
+// registers.
+// `between` runs once the tile's own words are out.
+template <int E, class Between>
 __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int64_t q, int lane, bool fresh,
-                                                 const float2 (&tot)[E], float (&hin)[E]) {
+                                                 const float2 (&tot)[E], float (&hin)[E], Between between) {
     constexpr int TC = 32 * E;
     constexpr int W = E == 1 ? 16 : 8;
     const int64_t step = p.n_strips * TC;                          // from a tile's words to the next chunk's
@@ -179,6 +187,7 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
     };
     if (fresh || q == 0) {
         publish_state();
+        between();
         return;
     }
     if (cut) {
@@ -187,6 +196,7 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
 #pragma unroll
         for (int e = 0; e < E; ++e) st_relaxed_u64(p.maps + at + e, pack_map(tot[e]));
     }
+    between();
     uint64_t m[W][E];
     uint32_t st[W][E];
 #pragma unroll
@@ -286,12 +296,47 @@ __device__ __forceinline__ void store_raw(void *base, int64_t off, typename Raw<
 }
 
 
-// The tiles of a block, handed from the carry warp to the data warps through
-// a ring: tile n lies in slot n % S, its table in s_info[n % (S + 1)] (read
-// until the tile's replay is over, one tile longer than the slot).
-template <int S> struct Ring {
-    uint64_t full[S];
-    TileInfo info[S + 1];
+// ------------------------------------------------------ inside a block
+//
+// Tile n of the block lies in slot n % S from its copies until every data
+// warp has replayed it; its maps and entering states in entry n % Q, Q =
+// lag + 1: a data warp folds tile n after its replay of tile n - Q, which it
+// began with that tile's states.  Every wait is bounded; one that runs out
+// poisons the tile (NaN) and records it, and nothing else waits on it.
+template <typename V, int S, int Q, int MAPS> struct Block {
+    uint64_t full[S], empty[S];            // copies and table there; replayed by every data warp
+    uint64_t maps[Q], in[Q];               // maps there; entering states there
+    TileInfo info[S];
+    V A[MAPS][Q][kWarps][32], B[MAPS][Q][kWarps][32];
+    V enter[MAPS][Q][kWarps][32];
+};
+template <class B, int S, int Q> __device__ __forceinline__ void init_block(B &blk) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(smem_addr(&blk.full[i]), 1);
+            mbar_init(smem_addr(&blk.empty[i]), kWarps);
+        }
+        for (int i = 0; i < Q; ++i) {
+            mbar_init(smem_addr(&blk.maps[i]), kWarps);
+            mbar_init(smem_addr(&blk.in[i]), 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// wait for use u of a barrier (its phases are uses 0, 1, 2, ...)
+struct Waiter {
+    uint32_t *status;
+    uint32_t limit;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, int u) {
+        if (mbar_wait(smem_addr(bar), uint32_t(u & 1), limit)) return true;
+        limit = 1;
+        if (status) atomicExch(status, 5u);                           // SGR_ERR_TIMEOUT
+        return false;
+    }
 };
 
 template <typename IO, int E, int OPS, int S, bool TMA>
@@ -299,243 +344,269 @@ struct SmemShape {
     static constexpr int TC = 32 * E;
     static constexpr uint32_t op_bytes = kTR * TC * sizeof(IO);
     static constexpr uint32_t slot_bytes = OPS * op_bytes;
-    static constexpr uint32_t bytes = TMA ? S * slot_bytes + 128 : 0;
+    static constexpr uint32_t ring_bytes = TMA ? S * slot_bytes : 0;
 };
 
-// The carry warp's side of the ring.  A tile is taken in three parts, so that
-// none of them delays the carry: next() draws its ticket, issue() starts its
-// copies as soon as the slot is free, finish() writes its table and lets the
-// data warps have it.  `reverse` counts chunks from the last.
-template <int S, int OPS, uint32_t OP_BYTES, int TC, bool TMA>
-struct Feed {
-    const GatedParams &p;
-    Ring<S> &ring;
-    const int lane;
-    const bool reverse;
-    const uint32_t slots;
-    const CUtensorMap *maps[3];
-    int64_t tile;                          // drawn, not yet finished; n_tiles: no more
-
-    __device__ __forceinline__ void next(bool first) {
-        if (p.ticket) {
-            if (!first && tile >= p.n_tiles) return;
+// The feeding warp: draws tickets, starts the copies of a tile when its slot
+// is free, writes its table and hands both over.  `reverse` counts chunks
+// from the last.  Ends with one entry for each carry warp whose tile is
+// n_tiles, so that each of them comes upon one.
+template <int S, int OPS, uint32_t OP_BYTES, int TC, bool TMA, class B>
+__device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slots, int lane, bool reverse,
+                                     const CUtensorMap *m0, const CUtensorMap *m1, const CUtensorMap *m2) {
+    Waiter wait{p.status, kTileWait};
+    int ends = 0;
+    for (int n = 0; ends < kCarryWarps; ++n) {
+        int64_t tile = p.n_tiles;
+        if (ends > 0) {
+        } else if (p.ticket) {
             uint32_t t = 0;
             if (lane == 0) t = atomicAdd(p.ticket, 1u) + 1u;
             tile = __shfl_sync(0xffffffffu, t, 0);
-        } else {
-            tile = first ? int64_t(blockIdx.x) : p.n_tiles;
+        } else if (n == 0) {
+            tile = blockIdx.x;
         }
-    }
-    __device__ __forceinline__ int64_t row0() const {
-        const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips);
-        return int64_t(reverse ? uint32_t(p.n_chunks) - 1 - q : q) * kTR;
-    }
-    __device__ __forceinline__ void issue(int n) {
-        if constexpr (TMA) {
-            if (lane == 0 && tile < p.n_tiles) {
-                const uint32_t strip = uint32_t(tile) % uint32_t(p.n_strips);
-                const uint32_t bar = smem_addr(&ring.full[n % S]);
-                const uint32_t dst = slots + uint32_t(n % S) * (OPS * OP_BYTES);
-                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(OPS * OP_BYTES)
-                             : "memory");
-#pragma unroll
-                for (int i = 0; i < OPS; ++i)
-                    tma_load_2d(dst + i * OP_BYTES, maps[i], int(strip) * TC, int(row0()), bar);
+        const bool more = tile < p.n_tiles;
+        if (n >= S) wait(&blk.empty[n % S], n / S - 1);
+        TileInfo &info = blk.info[n % S];
+        if (more) {
+            const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
+            const int64_t row0 = int64_t(reverse ? uint32_t(p.n_chunks) - 1 - q : q) * kTR;
+            if constexpr (TMA) {
+                if (lane == 0) {
+                    const uint32_t bar = smem_addr(&blk.full[n % S]);
+                    const uint32_t dst = slots + uint32_t(n % S) * (OPS * OP_BYTES);
+                    // the data warps' reads of the slot came before the copies into it
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(OPS * OP_BYTES)
+                                 : "memory");
+                    tma_load_2d(dst, m0, int(strip) * TC, int(row0), bar);
+                    tma_load_2d(dst + OP_BYTES, m1, int(strip) * TC, int(row0), bar);
+                    if constexpr (OPS == 3) tma_load_2d(dst + 2 * OP_BYTES, m2, int(strip) * TC, int(row0), bar);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            fill_info(p, row0, info, lane);
         }
-    }
-    __device__ __forceinline__ void finish(int n) {
-        TileInfo &info = ring.info[n % (S + 1)];
-        if (tile < p.n_tiles) fill_info(p, row0(), info, lane);
         if (lane == 0) info.tile = tile;
         __syncwarp();
-        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&ring.full[n % S])) : "memory");
+        if (lane == 0) arrive(&blk.full[n % S]);
+        if (!more) ++ends;
     }
-};
-
-// Data warp: wait for tile n.  The table is always there in the end (the
-// carry warp's own waits are bounded); false means that copies are missing,
-// and the tile's outputs become NaN.
-__device__ __forceinline__ bool wait_tile(uint64_t *full, int n, int S, uint32_t &limit, uint32_t *status) {
-    if (mbar_wait(smem_addr(&full[n % S]), uint32_t((n / S) & 1), limit)) return true;
-    limit = 1;
-    if (status) atomicExch(status, 5u);                               // SGR_ERR_TIMEOUT
-    return false;
-}
-constexpr uint32_t kTileWait = 1u << 24;
-
-struct RowMasks {
-    uint32_t starts, ends, live;           // bit r: row r of the warp starts / ends a sequence, lies in one
-};
-__device__ __forceinline__ RowMasks row_masks(const TileInfo &info, int64_t row0, int warp, int lane) {
-    const int rr = lane & 15;
-    RowMasks k;
-    k.starts = __ballot_sync(0xffffffffu, info.start[warp * kRows + rr] >= 0) & 0xffffu;
-    k.ends = __ballot_sync(0xffffffffu, info.end[warp * kRows + rr] >= 0) & 0xffffu;
-    k.live = __ballot_sync(0xffffffffu, row0 + rr >= info.lo && row0 + rr < info.hi) & 0xffffu;
-    return k;
 }
 
-// The carry warp's part of a tile once the data warps' maps are in shared
-// memory: the entering state of each warp.  DIR +1: warps in order, -1: from
-// the last.
-template <int E, int DIR, class V>
-__device__ __forceinline__ void carry_warps(const GatedParams &p, const V (&sA)[kWarps][32], const V (&sB)[kWarps][32],
-                                            V (&sin)[kWarps][32], int64_t strip, int64_t q, int lane, bool fresh,
-                                            float *entering, int64_t d0) {
-    float2 pre[kWarps][E], tot[E];
+// A carry warp: tiles c, c + kCarryWarps, ... of the block.  Forward (DIR +1):
+// warps in order; the state entering each chunk is kept in p.states if given.
+// Backward (DIR -1): warps from the last, and beside them (map 1) the states
+// of the forward recurrence within the tile, from p.states.
+template <int E, int S, int Q, int DIR, class B>
+__device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, int lane) {
+    Waiter wait{p.status, kTileWait};
+    for (int n = c;; n += kCarryWarps) {
+        wait(&blk.full[n % S], n / S);
+        const TileInfo &info = blk.info[n % S];
+        const int64_t tile = info.tile;
+        if (tile >= p.n_tiles) return;
+        const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
+        const bool fresh = DIR > 0 ? info.start[0] >= 0 : info.end[kTR - 1] >= 0;
+        const int e0 = n % Q;
+        const int64_t d0 = int64_t(strip) * 32 * E + lane * E;
+        float hf[E];
+        if constexpr (DIR < 0) {
+            const uint32_t chunk = uint32_t(p.n_chunks) - 1 - q;
+            const bool begins = info.start[0] >= 0 || chunk == 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) tot[e] = make_float2(1.f, 0.f);
+            for (int e = 0; e < E; ++e) hf[e] = begins || d0 + e >= p.D ? 0.f : p.states[int64_t(chunk) * p.D + d0 + e];
+        }
+        wait(&blk.maps[e0], n / Q);
+        auto map_of = [&](int k, int w, int e) {
+            return make_float2(reinterpret_cast<const float *>(&blk.A[k][e0][w][lane])[e],
+                               reinterpret_cast<const float *>(&blk.B[k][e0][w][lane])[e]);
+        };
+        // the states entering each warp from those entering the tile
+        auto enter = [&](int k, bool up, float (&h)[E]) {
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) {
-        const int w = DIR > 0 ? j : kWarps - 1 - j;
-        const float *A = reinterpret_cast<const float *>(&sA[w][lane]);
-        const float *B = reinterpret_cast<const float *>(&sB[w][lane]);
+            for (int j = 0; j < kWarps; ++j) {
+                const int w = up ? j : kWarps - 1 - j;
+                float *in = reinterpret_cast<float *>(&blk.enter[k][e0][w][lane]);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float2 m = map_of(k, w, e);
+                    in[e] = h[e];
+                    h[e] = apply_map(m.x, m.y, h[e]);
+                }
+            }
+        };
+        float2 tot[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            pre[j][e] = make_float2(A[e], B[e]);
-            tot[e] = then_map(tot[e], pre[j][e]);
+            tot[e] = map_of(0, DIR > 0 ? 0 : kWarps - 1, e);
+#pragma unroll
+            for (int j = 1; j < kWarps; ++j) tot[e] = then_map(tot[e], map_of(0, DIR > 0 ? j : kWarps - 1 - j, e));
+        }
+        float hin[E];
+        carry_tile_state<E>(p, strip, q, lane, fresh, tot, hin, [&] {
+            if constexpr (DIR < 0) enter(1, true, hf);
+        });
+        const float first[2] = {hin[0], hin[E - 1]};
+        enter(0, DIR > 0, hin);
+        __syncwarp();
+        if (lane == 0) arrive(&blk.in[e0]);
+        if constexpr (DIR > 0) {
+            if (p.states) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (d0 + e < p.D) p.states[q * p.D + d0 + e] = first[e];
+            }
         }
     }
-    float hin[E];
-    carry_tile_state<E>(p, strip, q, lane, fresh, tot, hin);
-    if (entering) {
+}
+
+// What a data warp knows of a tile: its place and, per row of the warp (bit
+// r), whether the row starts or ends a sequence and lies in one.
+struct WarpTile {
+    int64_t row0, d0;
+    uint32_t q, chunk;
+    uint32_t starts, ends, live;
+    int slot;
+    bool dvalid;
+};
+template <int TC>
+__device__ __forceinline__ WarpTile warp_tile(const GatedParams &p, const TileInfo &info, int slot, bool reverse, int warp,
+                                              int lane, int E) {
+    WarpTile t;
+    const uint32_t tile = uint32_t(info.tile);
+    t.slot = slot;
+    t.q = tile / uint32_t(p.n_strips);
+    t.chunk = reverse ? uint32_t(p.n_chunks) - 1 - t.q : t.q;
+    t.row0 = int64_t(t.chunk) * kTR + warp * kRows;
+    t.d0 = int64_t(tile - t.q * uint32_t(p.n_strips)) * TC + lane * E;
+    t.dvalid = t.d0 < p.D;
+    const int rr = lane & (kRows - 1);
+    constexpr uint32_t all = (1u << kRows) - 1u;
+    t.starts = __ballot_sync(0xffffffffu, info.start[warp * kRows + rr] >= 0) & all;
+    t.ends = __ballot_sync(0xffffffffu, info.end[warp * kRows + rr] >= 0) & all;
+    t.live = __ballot_sync(0xffffffffu, t.row0 + rr >= info.lo && t.row0 + rr < info.hi) & all;
+    return t;
+}
+
+// The thread's rows of operand OP of a tile: from the slot, or from memory
+// (read twice then, the second time from a cache).
+template <typename IO, int E, bool TMA, class Shape, int OP>
+__device__ __forceinline__ void tile_rows(const GatedParams &p, const unsigned char *smem, const WarpTile &t, int warp,
+                                          int lane, const void *base, int64_t rs, typename Raw<IO, E>::type (&x)[kRows]) {
+    using R = typename Raw<IO, E>::type;
+    if constexpr (TMA) {
+        const R *src = reinterpret_cast<const R *>(smem + t.slot * Shape::slot_bytes + OP * Shape::op_bytes) +
+                       warp * kRows * 32 + lane;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d0 + e < p.D) entering[q * p.D + d0 + e] = hin[e];
-    }
+        for (int r = 0; r < kRows; ++r) x[r] = src[r * 32];
+    } else {
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) {
-        const int w = DIR > 0 ? j : kWarps - 1 - j;
-        float *in = reinterpret_cast<float *>(&sin[w][lane]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            in[e] = hin[e];
-            hin[e] = apply_map(pre[j][e].x, pre[j][e].y, hin[e]);
+        for (int r = 0; r < kRows; ++r) {
+            const bool ok = t.dvalid && t.row0 + r < p.rows;
+            x[r] = ok ? *reinterpret_cast<const R *>(static_cast<const IO *>(base) + (t.row0 + r) * rs + t.d0) : R(0);
         }
     }
 }
 
 // ------------------------------------------------------------- forward
+template <typename IO, int E, bool TMA> struct ForwardShape {
+    using Ring = SmemShape<IO, E, 2, kSlots, TMA>;
+    using Blk = Block<typename FVec<E>::type, kSlots, kLag + 1, 1>;
+    static constexpr uint32_t smem_bytes = Ring::ring_bytes + sizeof(Blk);
+};
+
 template <typename IO, int E, int GATE, bool TMA>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_v) {
     using V = typename FVec<E>::type;
     using R = typename Raw<IO, E>::type;
     using C = Conv<IO, E>;
-    using Shape = SmemShape<IO, E, 2, kSlots, TMA>;
-    constexpr int TC = 32 * E;
+    using Shape = typename ForwardShape<IO, E, TMA>::Ring;
+    using Blk = typename ForwardShape<IO, E, TMA>::Blk;
+    constexpr int S = kSlots, Q = kLag + 1, TC = 32 * E;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Ring<kSlots> ring;
-    __shared__ V s_A[2][kWarps][32], s_B[2][kWarps][32], s_in[2][kWarps][32];
+    Blk &blk = *reinterpret_cast<Blk *>(smem + Shape::ring_bytes);
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kSlots; ++s) mbar_init(smem_addr(&ring.full[s]), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
+    init_block<Blk, S, Q>(blk);
     if (warp < kWarps) {
-        uint32_t limit = kTileWait;
-        for (int n = 0;; ++n) {
-            const int par = n & 1;
-            const bool got = wait_tile(ring.full, n, kSlots, limit, p.status);
-            const TileInfo &info = ring.info[n % (kSlots + 1)];
-            const int64_t tile = info.tile;
-            if (tile >= p.n_tiles) break;
-            const uint32_t chunk = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - chunk * uint32_t(p.n_strips);
-            const int64_t row0 = int64_t(chunk) * kTR + warp * kRows;
-            const int64_t d0 = int64_t(strip) * TC + lane * E;
-            const bool dvalid = d0 < p.D;
-            const RowMasks k = row_masks(info, row0, warp, lane);
-            R rf[kRows], rv[kRows];
-            if constexpr (TMA) {
-                const R *sf = reinterpret_cast<const R *>(smem + (n % kSlots) * Shape::slot_bytes) + warp * kRows * 32 + lane;
-                const R *sv = sf + kTR * 32;
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    rf[r] = sf[r * 32];
-                    rv[r] = sv[r * 32];
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const bool ok = dvalid && row0 + r < p.rows;
-                    rf[r] = ok ? load_raw<IO, E>(p.f, (row0 + r) * p.f_rs + d0) : R(0);
-                    rv[r] = ok ? load_raw<IO, E>(p.v, (row0 + r) * p.v_rs + d0) : R(0);
-                }
-            }
-            V a[kRows], b[kRows];
-            V A = vset<V>(1.f), B = vset<V>(0.f);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a[r], b[r]);
-                if (k.starts >> r & 1u) {
-                    A = vset<V>(-0.f);
-                    B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
-                }
-                B = vfma(a[r], B, b[r]);
-                A = vmul(A, a[r]);
-            }
-            if (!got) {
-                A = B = vset<V>(__int_as_float(0x7fffffff));
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) b[r] = B;
-            }
-            s_A[par][warp][lane] = A;
-            s_B[par][warp][lane] = B;
-            named_barrier_arrive(1 + par, kThreads);
-            named_barrier_sync(3 + par, kThreads);
-            V h = s_in[par][warp][lane];
-            char *dst = static_cast<char *>(p.h) + (row0 * p.h_rs + d0) * int64_t(sizeof(IO));
-            const int64_t pitch = p.h_rs * int64_t(sizeof(IO));
-            if (k.starts == 0u && k.ends == 0u && k.live == 0xffffu) {
-                if (dvalid) {
+        Waiter wait{p.status, kTileWait};
+        int n_end = 1 << 30;                               // tiles of the block, once known
+        for (int n = 0; n < n_end + kLag; ++n) {
+            if (n < n_end) {
+                const bool got = wait(&blk.full[n % S], n / S);
+                const TileInfo &info = blk.info[n % S];
+                if (info.tile >= p.n_tiles) {
+                    n_end = n;
+                } else {
+                    const WarpTile t = warp_tile<TC>(p, info, n % S, false, warp, lane, E);
+                    R rf[kRows], rv[kRows];
+                    tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
+                    tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
+                    V A = vset<V>(1.f), B = vset<V>(0.f);
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
-                        h = vfma(a[r], h, b[r]);
-                        __stcs(reinterpret_cast<R *>(dst), C::out(h));
-                        dst += pitch;
+                        V a, b;
+                        gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a, b);
+                        if (t.starts >> r & 1u) {
+                            A = vset<V>(-0.f);
+                            B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
+                        }
+                        B = vfma(a, B, b);
+                        A = vmul(A, a);
                     }
+                    if (!got) A = B = vset<V>(__int_as_float(0x7fffffff));
+                    blk.A[0][n % Q][warp][lane] = A;
+                    blk.B[0][n % Q][warp][lane] = B;
+                    __syncwarp();
+                    if (lane == 0) arrive(&blk.maps[n % Q]);
+                }
+            }
+            const int m = n - kLag;
+            if (m < 0 || m >= n_end) continue;
+            const bool got = wait(&blk.in[m % Q], m / Q);
+            const TileInfo &info = blk.info[m % S];
+            const WarpTile t = warp_tile<TC>(p, info, m % S, false, warp, lane, E);
+            R rf[kRows], rv[kRows];
+            tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
+            tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
+            V h = got ? blk.enter[0][m % Q][warp][lane] : vset<V>(__int_as_float(0x7fffffff));
+            char *dst = static_cast<char *>(p.h) + (t.row0 * p.h_rs + t.d0) * int64_t(sizeof(IO));
+            const int64_t pitch = p.h_rs * int64_t(sizeof(IO));
+            if (t.starts == 0u && t.ends == 0u && t.live == (1u << kRows) - 1u) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    V a, b;
+                    gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a, b);
+                    h = vfma(a, h, b);
+                    if (t.dvalid) __stcs(reinterpret_cast<R *>(dst), C::out(h));
+                    dst += pitch;
                 }
             } else {
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
-                    if (k.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
-                    h = vfma(a[r], h, b[r]);
-                    if (dvalid && row0 + r < p.rows) {
-                        if (k.live >> r & 1u) __stcs(reinterpret_cast<R *>(dst), C::out(h));
+                    V a, b;
+                    gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a, b);
+                    if (t.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
+                    h = vfma(a, h, b);
+                    if (t.dvalid && t.row0 + r < p.rows) {
+                        if (t.live >> r & 1u) __stcs(reinterpret_cast<R *>(dst), C::out(h));
                         else if (p.zero_padding) __stcs(reinterpret_cast<R *>(dst), R(0));
                     }
                     dst += pitch;
-                    if ((k.ends >> r & 1u) && p.h_last) put_state_row<E>(p.h_last, info.end[warp * kRows + r] * p.D, d0, p.D, h);
+                    if ((t.ends >> r & 1u) && p.h_last)
+                        put_state_row<E>(p.h_last, info.end[warp * kRows + r] * p.D, t.d0, p.D, h);
                 }
             }
+            __syncwarp();
+            if (lane == 0) arrive(&blk.empty[m % S]);
         }
+    } else if (warp < kWarps + kCarryWarps) {
+        carry_loop<E, S, Q, 1>(p, blk, warp - kWarps, lane);
     } else {
-        Feed<kSlots, 2, Shape::op_bytes, TC, TMA> feed{p, ring, lane, false, smem_addr(smem), {&map_f, &map_v, nullptr}, 0};
-        for (int n = 0; n < kSlots; ++n) {
-            feed.next(n == 0);
-            feed.issue(n);
-            feed.finish(n);
-        }
-        feed.next(false);
-        for (int n = 0;; ++n) {
-            const int par = n & 1;
-            const TileInfo &info = ring.info[n % (kSlots + 1)];
-            const int64_t tile = info.tile;
-            if (tile >= p.n_tiles) break;
-            const uint32_t chunk = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - chunk * uint32_t(p.n_strips);
-            const bool fresh = info.start[0] >= 0;
-            named_barrier_sync(1 + par, kThreads);         // the maps are there, and the slot has been read
-            feed.issue(n + kSlots);
-            carry_warps<E, 1>(p, s_A[par], s_B[par], s_in[par], strip, chunk, lane, fresh, p.states,
-                              int64_t(strip) * TC + lane * E);
-            named_barrier_arrive(3 + par, kThreads);
-            feed.finish(n + kSlots);
-            feed.next(false);
-        }
+        feed<S, 2, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, false, &map_f, &map_v, nullptr);
     }
     __syncthreads();
     empty_sequences(p, p.h_last, p.h0, p.h0_ss);
@@ -553,10 +624,6 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
 // D per kTR rows), instead of being read back: the outputs h are not needed,
 // so the pass reads three arrays and not four, and the states have not been
 // rounded to 16 bits.
-//
-// The tile's slot is read three times (folds, forward replay, reverse
-// replay), so it is refilled once the next tile's maps are in; the registers
-// hold the gates and the factors of df.
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ V bwd_gate(V f) {
     // GATE_SIGMOID: signed small probability; GATE_LOG: a, negated where f > 0, which has no gradient
@@ -567,181 +634,139 @@ __device__ __forceinline__ V bwd_gate(V f) {
             return x > 0.f ? -t : t;
         });
 }
+// (a, z) of it; z is 1 for GATE_LOG
 template <int GATE, class V>
-__device__ __forceinline__ V bwd_a(V s) {
+__device__ __forceinline__ void bwd_split(V s, V &a, V &z) {
     if constexpr (GATE == GATE_SIGMOID) {
-        V a, z;
         split_small(s, a, z);
-        return a;
     } else {
-        return vmap(s, [](float x) { return fabsf(x); });
+        a = vmap(s, [](float x) { return fabsf(x); });
+        z = vset<V>(1.f);
     }
 }
 
+template <typename IO, int E, bool TMA> struct BackwardShape {
+    using Ring = SmemShape<IO, E, 3, kBwdSlots, TMA>;
+    using Blk = Block<typename FVec<E>::type, kBwdSlots, kBwdLag + 1, 2>;       // maps 0: reverse, 1: forward
+    static constexpr uint32_t smem_bytes = Ring::ring_bytes + sizeof(Blk);
+};
+
 template <typename IO, int E, int GATE, bool TMA>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f,
                            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dh) {
     using V = typename FVec<E>::type;
     using R = typename Raw<IO, E>::type;
     using C = Conv<IO, E>;
-    using Shape = SmemShape<IO, E, 3, kBwdSlots, TMA>;
-    constexpr int TC = 32 * E;
+    using Shape = typename BackwardShape<IO, E, TMA>::Ring;
+    using Blk = typename BackwardShape<IO, E, TMA>::Blk;
+    constexpr int S = kBwdSlots, Q = kBwdLag + 1, TC = 32 * E;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Ring<kBwdSlots> ring;
-    __shared__ V s_A[kWarps][32], s_B[kWarps][32];                    // forward maps
-    __shared__ V s_RA[2][kWarps][32], s_RB[2][kWarps][32];            // reverse maps
-    __shared__ V s_in[2][kWarps][32];
+    Blk &blk = *reinterpret_cast<Blk *>(smem + Shape::ring_bytes);
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kBwdSlots; ++s) mbar_init(smem_addr(&ring.full[s]), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
+    init_block<Blk, S, Q>(blk);
     if (warp < kWarps) {
-        uint32_t limit = kTileWait;
-        for (int n = 0;; ++n) {
-            const int par = n & 1;
-            const bool got = wait_tile(ring.full, n, kBwdSlots, limit, p.status);
-            const TileInfo &info = ring.info[n % (kBwdSlots + 1)];
-            const int64_t tile = info.tile;
-            if (tile >= p.n_tiles) break;
-            const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
-            const uint32_t chunk = uint32_t(p.n_chunks) - 1 - q;
-            const int64_t row0 = int64_t(chunk) * kTR + warp * kRows;
-            const int64_t d0 = int64_t(strip) * TC + lane * E;
-            const bool dvalid = d0 < p.D;
-            V h = info.start[0] >= 0 || chunk == 0 ? vset<V>(0.f) : state_row<E>(p.states, chunk * p.D, d0, p.D);
-            const RowMasks k = row_masks(info, row0, warp, lane);
-            [[maybe_unused]] R gv[TMA ? 1 : kRows], gg[TMA ? 1 : kRows];
-            const R *sf = reinterpret_cast<const R *>(smem + (n % kBwdSlots) * Shape::slot_bytes) + warp * kRows * 32 + lane;
-            if constexpr (!TMA) {
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const bool ok = dvalid && row0 + r < p.rows;
-                    gv[r] = ok ? load_raw<IO, E>(p.v, (row0 + r) * p.v_rs + d0) : R(0);
-                    gg[r] = ok ? load_raw<IO, E>(p.dh, (row0 + r) * p.dh_rs + d0) : R(0);
-                }
-            }
-            auto in_f = [&](int r) {
-                if constexpr (TMA) return C::in(sf[r * 32]);
-                else return C::in(dvalid && row0 + r < p.rows ? load_raw<IO, E>(p.f, (row0 + r) * p.f_rs + d0) : R(0));
-            };
-            auto in_v = [&](int r) {
-                if constexpr (TMA) return C::in(sf[(kTR + r) * 32]);
-                else return C::in(gv[r]);
-            };
-            auto in_g = [&](int r) {
-                if constexpr (TMA) return C::in(sf[(2 * kTR + r) * 32]);
-                else return C::in(gg[r]);
-            };
-            V s[kRows];
-            V A = vset<V>(1.f), B = vset<V>(0.f);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                s[r] = bwd_gate<GATE, IO>(in_f(r));
-                V a, b = in_v(r);
-                if constexpr (GATE == GATE_SIGMOID) {
-                    V z;
-                    split_small(s[r], a, z);
-                    b = vmul(z, b);
+        Waiter wait{p.status, kTileWait};
+        int n_end = 1 << 30;
+        for (int n = 0; n < n_end + kBwdLag; ++n) {
+            if (n < n_end) {
+                const bool got = wait(&blk.full[n % S], n / S);
+                const TileInfo &info = blk.info[n % S];
+                if (info.tile >= p.n_tiles) {
+                    n_end = n;
                 } else {
-                    a = bwd_a<GATE>(s[r]);
-                }
-                if (k.starts >> r & 1u) {
-                    A = vset<V>(-0.f);
-                    B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
-                }
-                B = vfma(a, B, b);
-                A = vmul(A, a);
-            }
-            V RA = vset<V>(1.f), RB = vset<V>(0.f);
+                    const WarpTile t = warp_tile<TC>(p, info, n % S, true, warp, lane, E);
+                    R rf[kRows], rv[kRows], rg[kRows];
+                    tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
+                    tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
+                    tile_rows<IO, E, TMA, Shape, 2>(p, smem, t, warp, lane, p.dh, p.dh_rs, rg);
+                    V a[kRows];
+                    V A = vset<V>(1.f), B = vset<V>(0.f);
 #pragma unroll
-            for (int r = kRows - 1; r >= 0; --r) {
-                const V a = bwd_a<GATE>(s[r]);
-                if (k.ends >> r & 1u) {
-                    RA = vset<V>(-0.f);
-                    RB = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, d0, p.D);
-                }
-                RB = vmul(a, vadd(RB, in_g(r)));
-                RA = vmul(RA, a);
-            }
-            if (!got) {
-                A = B = RA = RB = vset<V>(__int_as_float(0x7fffffff));
+                    for (int r = 0; r < kRows; ++r) {
+                        V b;
+                        gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a[r], b);
+                        if (t.starts >> r & 1u) {
+                            A = vset<V>(-0.f);
+                            B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
+                        }
+                        B = vfma(a[r], B, b);
+                        A = vmul(A, a[r]);
+                    }
+                    V RA = vset<V>(1.f), RB = vset<V>(0.f);
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) s[r] = B;
+                    for (int r = kRows - 1; r >= 0; --r) {
+                        if (t.ends >> r & 1u) {
+                            RA = vset<V>(-0.f);
+                            RB = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, t.d0, p.D);
+                        }
+                        RB = vmul(a[r], vadd(RB, C::in(rg[r])));
+                        RA = vmul(RA, a[r]);
+                    }
+                    if (!got) A = B = RA = RB = vset<V>(__int_as_float(0x7fffffff));
+                    blk.A[0][n % Q][warp][lane] = RA;
+                    blk.B[0][n % Q][warp][lane] = RB;
+                    blk.A[1][n % Q][warp][lane] = A;
+                    blk.B[1][n % Q][warp][lane] = B;
+                    __syncwarp();
+                    if (lane == 0) arrive(&blk.maps[n % Q]);
+                }
             }
-            s_A[warp][lane] = A;
-            s_B[warp][lane] = B;
-            s_RA[par][warp][lane] = RA;
-            s_RB[par][warp][lane] = RB;
-            named_barrier_arrive(1 + par, kThreads);
-            named_barrier_sync(5, kWarps * 32);                       // the data warps' maps are there
-            for (int w = 0; w < warp; ++w)
-                h = vmap(s_A[w][lane], s_B[w][lane], h, [](float x, float y, float z) { return apply_map(x, y, z); });
-            V c[kRows];                                               // df = c g
+            const int m = n - kBwdLag;
+            if (m < 0 || m >= n_end) continue;
+            const TileInfo &info = blk.info[m % S];
+            const WarpTile t = warp_tile<TC>(p, info, m % S, true, warp, lane, E);
+            R rv[kRows], rg[kRows];
+            V s[kRows], c[kRows];                                     // df = c g
+            {
+                R rf[kRows];
+                tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) s[r] = bwd_gate<GATE, IO>(C::in(rf[r]));
+            }
+            tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
+            const bool got = wait(&blk.in[m % Q], m / Q);
+            V h = blk.enter[1][m % Q][warp][lane];
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                if (k.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, d0, p.D);
-                const V v = in_v(r);
+                if (t.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
+                const V v = C::in(rv[r]);
+                V a, z;
+                bwd_split<GATE>(s[r], a, z);
                 if constexpr (GATE == GATE_SIGMOID) {
-                    V a, z;
-                    split_small(s[r], a, z);
                     c[r] = vmul(vmul(a, z), vfma(v, vset<V>(-1.f), h));
                     h = vfma(a, h, vmul(z, v));
                 } else {
                     c[r] = vmap(s[r], h, [](float x, float y) { return is_cut(x) ? 0.f : x * y; });
-                    h = vfma(bwd_a<GATE>(s[r]), h, v);
+                    h = vfma(a, h, v);
                 }
             }
-            named_barrier_sync(3 + par, kThreads);
-            V flow = s_in[par][warp][lane];
+            tile_rows<IO, E, TMA, Shape, 2>(p, smem, t, warp, lane, p.dh, p.dh_rs, rg);
+            V flow = got ? blk.enter[0][m % Q][warp][lane] : vset<V>(__int_as_float(0x7fffffff));
 #pragma unroll
             for (int r = kRows - 1; r >= 0; --r) {
-                if (k.ends >> r & 1u) flow = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, d0, p.D);
-                const V g = vadd(flow, in_g(r));
-                V a, dv = g;
-                if constexpr (GATE == GATE_SIGMOID) {
-                    V z;
-                    split_small(s[r], a, z);
-                    dv = vmul(z, g);
-                } else {
-                    a = bwd_a<GATE>(s[r]);
-                }
-                if (dvalid && row0 + r < p.rows) {
-                    const bool live = k.live >> r & 1u;
-                    store_raw<IO, E>(p.df, (row0 + r) * p.df_rs + d0, live ? C::out(vmul(c[r], g)) : R(0));
-                    store_raw<IO, E>(p.dv, (row0 + r) * p.dv_rs + d0, live ? C::out(dv) : R(0));
+                if (t.ends >> r & 1u) flow = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, t.d0, p.D);
+                const V g = vadd(flow, C::in(rg[r]));
+                V a, z;
+                bwd_split<GATE>(s[r], a, z);
+                if (t.dvalid && t.row0 + r < p.rows) {
+                    const bool live = t.live >> r & 1u;
+                    store_raw<IO, E>(p.df, (t.row0 + r) * p.df_rs + t.d0, live ? C::out(vmul(c[r], g)) : R(0));
+                    store_raw<IO, E>(p.dv, (t.row0 + r) * p.dv_rs + t.d0,
+                                     live ? C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g) : R(0));
                 }
                 flow = vmul(a, g);
-                if ((k.starts >> r & 1u) && p.dh0) put_state_row<E>(p.dh0, info.start[warp * kRows + r] * p.D, d0, p.D, flow);
+                if ((t.starts >> r & 1u) && p.dh0)
+                    put_state_row<E>(p.dh0, info.start[warp * kRows + r] * p.D, t.d0, p.D, flow);
             }
+            __syncwarp();
+            if (lane == 0) arrive(&blk.empty[m % S]);
         }
+    } else if (warp < kWarps + kCarryWarps) {
+        carry_loop<E, S, Q, -1>(p, blk, warp - kWarps, lane);
     } else {
-        Feed<kBwdSlots, 3, Shape::op_bytes, TC, TMA> feed{p, ring, lane, true, smem_addr(smem), {&map_f, &map_v, &map_dh}, 0};
-        for (int n = 0; n < kBwdSlots; ++n) {
-            feed.next(n == 0);
-            feed.issue(n);
-            feed.finish(n);
-        }
-        feed.next(false);
-        for (int n = 0;; ++n) {
-            const int par = n & 1;
-            const TileInfo &info = ring.info[n % (kBwdSlots + 1)];
-            const int64_t tile = info.tile;
-            if (tile >= p.n_tiles) break;
-            const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
-            const bool fresh = info.end[kTR - 1] >= 0;
-            named_barrier_sync(1 + par, kThreads);         // every data warp has left tile n - 1 behind
-            if (n >= 1) feed.issue(n + kBwdSlots - 1);     // ... whose slot takes this one
-            carry_warps<E, -1>(p, s_RA[par], s_RB[par], s_in[par], strip, q, lane, fresh, nullptr, 0);
-            named_barrier_arrive(3 + par, kThreads);
-            if (n >= 1) {
-                feed.finish(n + kBwdSlots - 1);
-                feed.next(false);
-            }
-        }
+        feed<S, 3, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, true, &map_f, &map_v, &map_dh);
     }
     __syncthreads();
     empty_sequences(p, p.dh0, p.dh_last, p.D);

@@ -17,7 +17,7 @@ namespace sgr {
 namespace i8 {
 
 constexpr int kKB = 128;                       // K bytes per stage
-constexpr uint32_t kWait = 1u << 20;
+constexpr uint32_t kWait = 1u << 16;        // polls of a wait (each suspends for tens of us)
 
 // kind::i8 instruction descriptor: s8 x s8 -> s32, both K-major
 constexpr uint32_t idesc(int m, int n) {

@@ -11,7 +11,7 @@ from scan_gated_rnns_b200 import _abi, gated, int8, ops
 from gated_reference import grad64, scan64
 from test_abi import fake_addresses
 
-TR = 112                                     # rows per tile of the kernels
+TR = 104                                     # rows per tile of the kernels
 
 
 # ------------------------------------------------------------- reference
