@@ -27,10 +27,10 @@ struct Layout {
     int64_t n_strips, n_chunks, n_tiles;
     size_t maps, carry, total;
 };
-Layout layout(int64_t rows, int64_t D, int tc) {
+Layout layout(int64_t rows, int64_t D, int tc, int tr) {
     Layout l;
     l.n_strips = (D + tc - 1) / tc;
-    l.n_chunks = (rows + kTR - 1) / kTR;
+    l.n_chunks = (rows + tr - 1) / tr;
     l.n_tiles = l.n_strips * l.n_chunks;
     l.maps = kHeader;
     l.carry = l.maps + size_t(l.n_tiles) * tc * 8;
@@ -42,17 +42,17 @@ bool sizes_ok(int64_t rows, int64_t D) {
     int64_t n = 0;
     // 16 bytes an element covers the workspace and every dense array
     return rows <= kMaxRows && D <= (int64_t(1) << 31) - 64 && host::mul_ok(rows, D, &n) && host::mul_ok(n, 16, &n) &&
-           ((rows + kTR - 1) / kTR) * ((D + 31) / 32) <= std::numeric_limits<int>::max();
+           ((rows + kBwdTR - 1) / kBwdTR) * ((D + 31) / 32) <= std::numeric_limits<int>::max();
 }
 
-// Tensor map of (rows, D) for boxes of 128 bytes x kTR rows; what lies past
+// Tensor map of (rows, D) for boxes of 128 bytes x tr rows; what lies past
 // the edges reads as zero.
-bool tile_map(CUtensorMap *map, const void *base, int64_t rows, int64_t D, int64_t rs, int esz) {
+bool tile_map(CUtensorMap *map, const void *base, int64_t rows, int64_t D, int64_t rs, int esz, int tr) {
     const host::EncodeTiledFn enc = host::encode_tiled();
     if (!enc) return false;
     const cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {rows > 1 ? cuuint64_t(rs) * esz : align_up(size_t(D) * esz, 16)};
-    const cuuint32_t box[2] = {cuuint32_t(128 / esz), cuuint32_t(kTR)};
+    const cuuint32_t box[2] = {cuuint32_t(128 / esz), cuuint32_t(tr)};
     const cuuint32_t es[2] = {1u, 1u};
     return enc(map, esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
                const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -75,8 +75,9 @@ cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
     CUtensorMap m[3];
     std::memset(m, 0, sizeof(m));
     if (TMA) {
-        if (!tile_map(&m[0], p.f, p.rows, p.D, p.f_rs, sizeof(IO)) || !tile_map(&m[1], p.v, p.rows, p.D, p.v_rs, sizeof(IO)) ||
-            (backward && !tile_map(&m[2], p.dh, p.rows, p.D, p.dh_rs, sizeof(IO))))
+        const int esz = sizeof(IO), tr = backward ? kBwdTR : kTR;
+        if (!tile_map(&m[0], p.f, p.rows, p.D, p.f_rs, esz, tr) || !tile_map(&m[1], p.v, p.rows, p.D, p.v_rs, esz, tr) ||
+            (backward && !tile_map(&m[2], p.dh, p.rows, p.D, p.dh_rs, esz, tr)))
             return cudaErrorInvalidValue;
     }
     if (backward) {
@@ -128,7 +129,8 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
     if (p.D == 0 || (p.rows == 0 && p.n_seqs == 0)) return SGR_OK;
     if (p.f_rs < 0 || p.v_rs < 0 || p.h_rs < 0 || p.dh_rs < 0 || p.df_rs < 0 || p.dv_rs < 0) return SGR_ERR_INVALID_ARG;
     if (!sizes_ok(p.rows, p.D) || p.n_seqs > std::numeric_limits<int>::max()) return SGR_ERR_UNSUPPORTED;
-    const int64_t n_chunks = (p.rows + kTR - 1) / kTR;
+    const int tr = backward ? kBwdTR : kTR;
+    const int64_t n_chunks = (p.rows + tr - 1) / tr, n_states = (p.rows + kBwdTR - 1) / kBwdTR;
     if (p.rows > 0) {
         if (!p.f || !p.v) return SGR_ERR_INVALID_ARG;
         if (backward ? (!p.dh || !p.df || !p.dv || (n_chunks > 1 && !p.states)) : !p.h) return SGR_ERR_INVALID_ARG;
@@ -140,7 +142,7 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
         !host::span_ok(p.rows, p.D, p.dh_rs, esz, &b_dh) || !host::span_ok(p.rows, p.D, p.h_rs, esz, &b_h) ||
         !host::span_ok(p.rows, p.D, p.df_rs, esz, &b_df) || !host::span_ok(p.rows, p.D, p.dv_rs, esz, &b_dv) ||
         !host::span_ok(p.n_seqs, p.D, p.h0_ss, 4, &b_h0) || !host::span_ok(p.n_seqs, p.D, p.D, 4, &b_seq) ||
-        !host::mul_ok(p.n_seqs + 1, p.cu_bytes, &b_cu) || !host::span_ok(n_chunks, p.D, p.D, 4, &b_st))
+        !host::mul_ok(p.n_seqs + 1, p.cu_bytes, &b_cu) || !host::span_ok(n_states, p.D, p.D, 4, &b_st))
         return SGR_ERR_UNSUPPORTED;
     // Two channels a thread where every row starts on a 4-byte boundary.
     int E = 1;
@@ -152,7 +154,7 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
             four = four && host::aligned(q, 4);
         E = (odd & 1) == 0 && four ? 2 : 1;
     }
-    const Layout l = layout(p.rows, p.D, 32 * E);
+    const Layout l = layout(p.rows, p.D, 32 * E, tr);
     p.n_strips = l.n_strips;
     p.n_chunks = l.n_chunks;
     p.n_tiles = l.n_tiles;
@@ -199,11 +201,11 @@ void launch_step(const StepParams &p, int gate, unsigned grid, cudaStream_t s) {
 
 extern "C" {
 
-int64_t sgr_gated_chunks(int64_t rows) { return rows <= 0 ? 0 : (rows + kTR - 1) / kTR; }
+int64_t sgr_gated_chunks(int64_t rows) { return rows <= 0 ? 0 : (rows + kBwdTR - 1) / kBwdTR; }
 
 size_t sgr_gated_workspace_size(int64_t rows, int64_t D) {
-    if (rows <= kTR || D <= 0 || !sizes_ok(rows, D)) return 0;
-    return std::max(layout(rows, D, 32).total, layout(rows, D, 64).total);
+    if (rows <= kBwdTR || D <= 0 || !sizes_ok(rows, D)) return 0;
+    return std::max(layout(rows, D, 32, kBwdTR).total, layout(rows, D, 64, kBwdTR).total);
 }
 
 sgr_status_t gated_scan(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride, const float *h0,

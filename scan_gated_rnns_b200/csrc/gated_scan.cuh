@@ -9,8 +9,8 @@
 // sign), and is never multiplied with what came before, so nothing that an
 // earlier sequence held (infinities, NaN) reaches a later one.
 //
-// A tile is kTR rows x TC channels (128 bytes of a row).  Data warp w owns
-// rows [8 w, 8 w + 8), lane l channels [E l, E l + E): a thread folds its 8
+// A tile is TR rows x TC channels (128 bytes of a row).  Each data warp owns R
+// consecutive rows of it, lane l channels [E l, E l + E): a thread folds its
 // rows, the folds of a channel meet in shared memory, and a carry warp finds
 // the state that enters the tile; the threads then replay their rows from it.
 // Inputs are read from memory once and outputs written once.
@@ -31,10 +31,12 @@
 // on 16-byte boundaries, else the data warps load from memory themselves) and
 // writes each tile's table of sequence starts and ends.  A tile's state takes
 // two or three microseconds to arrive, longer than its arithmetic, so the
-// data warps fold tile n and then replay tile n - kLag, evaluating its gates
-// again from the ring: the second evaluation costs less than holding two
-// values per element in registers across the wait, which left room for two
-// tiles per SM only (bf16 32768 x 4096, sigmoid: 307 us that way).
+// data warps fold tile n and then replay tile n - 1.  Across the wait a thread
+// keeps one register per element, the gate; the values are read again from
+// the ring.  (Both coefficients in registers left room for one tile at a time
+// in each of two blocks per SM, which spent half its time waiting, 307 us on
+// bf16 32768 x 4096; evaluating the gates twice was bound by instruction
+// issue, 50 per element, 311 us.)
 #pragma once
 
 #include "gated_math.cuh"
@@ -42,14 +44,16 @@
 namespace sgr {
 namespace gated {
 
-constexpr int kWarps = 13;                 // data warps
-constexpr int kRows = 8;                   // rows per data warp and thread
-constexpr int kTR = kWarps * kRows;        // rows per tile, and between saved states
+constexpr int kWarps = 12;                 // data warps
 constexpr int kCarryWarps = 2;             // tiles in turn
 constexpr int kThreads = (kWarps + kCarryWarps + 1) * 32;   // the last warp feeds the ring
-constexpr int kSlots = 6, kLag = 2;        // forward: tiles in shared memory, tiles between fold and replay
-constexpr int kBwdSlots = 4, kBwdLag = 1;  // backward
+constexpr int kRows = 16, kBwdRows = 8;    // rows per data warp and thread, forward and backward
+constexpr int kTR = kWarps * kRows;        // rows per forward tile
+constexpr int kBwdTR = kWarps * kBwdRows;  // rows per backward tile, and between saved states
+constexpr int kSlots = 4, kBwdSlots = 5;   // tiles in shared memory
+constexpr int kQ = 2;                      // tiles between fold and the end of their replay
 constexpr uint32_t kTileWait = 1u << 16;   // polls of a wait inside the block (each suspends for tens of us)
+static_assert(kTR == 2 * kBwdTR, "a forward tile holds two saved states");
 constexpr uint32_t kNone = 0xffffffffu;    // a word not yet published
 
 struct GatedParams {
@@ -62,7 +66,7 @@ struct GatedParams {
     float *h_last;                         // (n_seqs, D) or null
     const float *dh_last;                  // (n_seqs, D) or null
     float *dh0;                            // (n_seqs, D) or null
-    float *states;                         // (n_chunks, D): state entering each chunk, or null (forward)
+    float *states;                         // (ceil(rows / kBwdTR), D): state entering each, or null (forward)
     const void *cu;                        // n_seqs + 1 row bounds, or null: sequences of seq_rows rows
     int cu_bytes;                          // 4 or 8
     uint32_t seq_rows;
@@ -87,62 +91,80 @@ __device__ __forceinline__ float2 then_map(float2 first, float2 then) {
     return is_cut(then.x) ? then : make_float2(first.x * then.x, fmaf(then.x, first.y, then.y));
 }
 
-// What the carry warp tells the data warps of a tile.
-struct TileInfo {
-    int64_t tile;
-    int64_t lo, hi;                        // rows that lie in sequences
-    int start[kTR], end[kTR];              // sequence that starts (ends) at the row, or -1
+// What the feeding warp tells the others of a tile.
+template <int TR> struct TileInfo {
+    int64_t tile, row0;                    // tile n_tiles: no more
+    int strip, q;                          // its strip, and its place along it in processing order
+    uint4 masks[kWarps];                   // of each data warp's rows: starts, ends, in a sequence; .w: all plain
+    int start[TR], end[TR];                // sequence that starts (ends) at the row, or -1
 };
 
-// Fill the table of the tile of rows [row0, row0 + kTR) (whole warp).  Bounds
+// Fill the table of the tile of rows [row0, row0 + TR) (whole warp).  Bounds
 // that are not ascending give wrong sequences but never a row or a sequence
 // outside the buffers.
-__device__ __forceinline__ void fill_info(const GatedParams &p, int64_t row0, TileInfo &t, int lane) {
-    const int64_t row_end = row0 + kTR < p.rows ? row0 + kTR : p.rows;
+template <int TR>
+__device__ __forceinline__ void fill_info(const GatedParams &p, int64_t row0, TileInfo<TR> &t, int lane) {
+    constexpr int R = TR / kWarps;
+    const int64_t row_end = row0 + TR < p.rows ? row0 + TR : p.rows;
+    int64_t lo_row = 0, hi_row = p.rows;   // rows that lie in sequences
     if (p.cu == nullptr) {
-        for (int r = lane; r < kTR; r += 32) {
-            const uint32_t n = uint32_t(row0 + r), s = n / p.seq_rows, k = n - s * p.seq_rows;
+        uint32_t s = uint32_t(row0 + lane) / p.seq_rows, k = uint32_t(row0 + lane) - s * p.seq_rows;
+        for (int r = lane; r < TR; r += 32) {
             const bool in = row0 + r < p.rows;
             t.start[r] = in && k == 0 ? int(s) : -1;
             t.end[r] = in && k + 1 == p.seq_rows ? int(s) : -1;
-        }
-        if (lane == 0) { t.lo = 0; t.hi = p.rows; }
-        __syncwarp();
-        return;
-    }
-    for (int r = lane; r < kTR; r += 32) t.start[r] = t.end[r] = -1;
-    if (lane == 0) {
-        const int64_t lo = cu_at(p, 0), hi = cu_at(p, p.n_seqs);
-        t.lo = lo;
-        t.hi = hi < p.rows ? hi : p.rows;
-    }
-    // bounds at or below row0, by a 33-way search: the last of them begins the
-    // sequence that holds row0
-    int64_t lo = 0, hi = p.n_seqs + 1;
-    while (lo < hi) {
-        const int64_t step = (hi - lo + 31) / 32;
-        const int64_t i = lo + (lane + 1) * step - 1;
-        const bool below = i < hi && cu_at(p, i) <= row0;
-        const int n = __popc(__ballot_sync(0xffffffffu, below));
-        const int64_t next = lo + n * step;
-        const int64_t top = lo + (n + 1) * step - 1;
-        lo = next < hi ? next : hi;
-        hi = top < hi ? top : hi;
-    }
-    __syncwarp();
-    for (int64_t s = (lo > 0 ? lo - 1 : 0) + lane;; s += 32) {
-        bool more = false;
-        if (s < p.n_seqs) {
-            const int64_t b = cu_at(p, s), e = cu_at(p, s + 1);
-            more = b < row_end;
-            if (b < e) {
-                if (b >= row0 && b < row_end) t.start[b - row0] = int(s);
-                if (e > row0 && e <= row_end) t.end[e - 1 - row0] = int(s);
+            k += 32;
+            if (k >= p.seq_rows) {
+                const uint32_t over = k / p.seq_rows;
+                s += over;
+                k -= over * p.seq_rows;
             }
         }
-        if (!__any_sync(0xffffffffu, more)) break;
+    } else {
+        for (int r = lane; r < TR; r += 32) t.start[r] = t.end[r] = -1;
+        lo_row = cu_at(p, 0);
+        const int64_t last = cu_at(p, p.n_seqs);
+        hi_row = last < p.rows ? last : p.rows;
+        // bounds at or below row0, by a 33-way search: the last of them begins the
+        // sequence that holds row0
+        int64_t lo = 0, hi = p.n_seqs + 1;
+        while (lo < hi) {
+            const int64_t step = (hi - lo + 31) / 32;
+            const int64_t i = lo + (lane + 1) * step - 1;
+            const bool below = i < hi && cu_at(p, i) <= row0;
+            const int n = __popc(__ballot_sync(0xffffffffu, below));
+            const int64_t next = lo + n * step;
+            const int64_t top = lo + (n + 1) * step - 1;
+            lo = next < hi ? next : hi;
+            hi = top < hi ? top : hi;
+        }
+        __syncwarp();
+        for (int64_t s = (lo > 0 ? lo - 1 : 0) + lane;; s += 32) {
+            bool more = false;
+            if (s < p.n_seqs) {
+                const int64_t b = cu_at(p, s), e = cu_at(p, s + 1);
+                more = b < row_end;
+                if (b < e) {
+                    if (b >= row0 && b < row_end) t.start[b - row0] = int(s);
+                    if (e > row0 && e <= row_end) t.end[e - 1 - row0] = int(s);
+                }
+            }
+            if (!__any_sync(0xffffffffu, more)) break;
+        }
     }
     __syncwarp();
+#pragma unroll
+    for (int r0 = 0; r0 < TR; r0 += 32) {
+        const int r = r0 + lane;
+        const uint32_t starts = __ballot_sync(0xffffffffu, r < TR && t.start[r < TR ? r : 0] >= 0);
+        const uint32_t ends = __ballot_sync(0xffffffffu, r < TR && t.end[r < TR ? r : 0] >= 0);
+        const uint32_t live = __ballot_sync(0xffffffffu, r < TR && row0 + r >= lo_row && row0 + r < hi_row);
+        if (lane < 32 / R && r0 / R + lane < kWarps) {
+            constexpr uint32_t all = (1u << R) - 1u;
+            const uint32_t a = starts >> (lane * R) & all, b = ends >> (lane * R) & all, c = live >> (lane * R) & all;
+            t.masks[r0 / R + lane] = make_uint4(a, b, c, a == 0u && b == 0u && c == all);
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t ld_relaxed_u32(const uint32_t *p) {
@@ -283,40 +305,27 @@ __device__ __forceinline__ void put_state_row(float *base, int64_t off, int64_t 
     }
 }
 
-// Streaming load and store of one thread's E channels of a row.  E = 2 is
-// chosen only for even D, strides and 4-byte aligned bases, so a pair never
-// straddles the last channel.
-template <typename IO, int E>
-__device__ __forceinline__ typename Raw<IO, E>::type load_raw(const void *base, int64_t off) {
-    return __ldcs(reinterpret_cast<const typename Raw<IO, E>::type *>(static_cast<const IO *>(base) + off));
-}
-template <typename IO, int E>
-__device__ __forceinline__ void store_raw(void *base, int64_t off, typename Raw<IO, E>::type x) {
-    __stcs(reinterpret_cast<typename Raw<IO, E>::type *>(static_cast<IO *>(base) + off), x);
-}
-
-
 // ------------------------------------------------------ inside a block
 //
 // Tile n of the block lies in slot n % S from its copies until every data
-// warp has replayed it; its maps and entering states in entry n % Q, Q =
-// lag + 1: a data warp folds tile n after its replay of tile n - Q, which it
-// began with that tile's states.  Every wait is bounded; one that runs out
-// poisons the tile (NaN) and records it, and nothing else waits on it.
-template <typename V, int S, int Q, int MAPS> struct Block {
+// warp has replayed it; its maps and entering states in entry n % kQ: a data
+// warp folds tile n after its replay of tile n - 2, which it began with that
+// tile's states.  Every wait is bounded; one that runs out poisons the tile
+// (NaN) and records it, and nothing else waits on it.
+template <typename V, int S, int TR, int MAPS> struct Block {
     uint64_t full[S], empty[S];            // copies and table there; replayed by every data warp
-    uint64_t maps[Q], in[Q];               // maps there; entering states there
-    TileInfo info[S];
-    V A[MAPS][Q][kWarps][32], B[MAPS][Q][kWarps][32];
-    V enter[MAPS][Q][kWarps][32];
+    uint64_t maps[kQ], in[kQ];             // maps there; entering states there
+    TileInfo<TR> info[S];
+    V A[MAPS][kQ][kWarps][32], B[MAPS][kQ][kWarps][32];
+    V enter[MAPS][kQ][kWarps][32];
 };
-template <class B, int S, int Q> __device__ __forceinline__ void init_block(B &blk) {
+template <int S, class B> __device__ __forceinline__ void init_block(B &blk) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(smem_addr(&blk.full[i]), 1);
             mbar_init(smem_addr(&blk.empty[i]), kWarps);
         }
-        for (int i = 0; i < Q; ++i) {
+        for (int i = 0; i < kQ; ++i) {
             mbar_init(smem_addr(&blk.maps[i]), kWarps);
             mbar_init(smem_addr(&blk.in[i]), 1);
         }
@@ -338,20 +347,22 @@ struct Waiter {
         return false;
     }
 };
+__device__ __forceinline__ float nan_value() { return __int_as_float(0x7fffffff); }
 
-template <typename IO, int E, int OPS, int S, bool TMA>
+template <typename IO, int E, int OPS, int S, int TR, bool TMA>
 struct SmemShape {
     static constexpr int TC = 32 * E;
-    static constexpr uint32_t op_bytes = kTR * TC * sizeof(IO);
+    static constexpr uint32_t op_bytes = TR * TC * sizeof(IO);
     static constexpr uint32_t slot_bytes = OPS * op_bytes;
     static constexpr uint32_t ring_bytes = TMA ? S * slot_bytes : 0;
+    static_assert(op_bytes % 128 == 0 && TR <= 256, "copy boxes");
 };
 
 // The feeding warp: draws tickets, starts the copies of a tile when its slot
 // is free, writes its table and hands both over.  `reverse` counts chunks
 // from the last.  Ends with one entry for each carry warp whose tile is
 // n_tiles, so that each of them comes upon one.
-template <int S, int OPS, uint32_t OP_BYTES, int TC, bool TMA, class B>
+template <int S, int OPS, int TR, uint32_t OP_BYTES, int TC, bool TMA, class B>
 __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slots, int lane, bool reverse,
                                      const CUtensorMap *m0, const CUtensorMap *m1, const CUtensorMap *m2) {
     Waiter wait{p.status, kTileWait};
@@ -368,10 +379,10 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
         }
         const bool more = tile < p.n_tiles;
         if (n >= S) wait(&blk.empty[n % S], n / S - 1);
-        TileInfo &info = blk.info[n % S];
+        TileInfo<TR> &info = blk.info[n % S];
         if (more) {
             const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
-            const int64_t row0 = int64_t(reverse ? uint32_t(p.n_chunks) - 1 - q : q) * kTR;
+            const int64_t row0 = int64_t(reverse ? uint32_t(p.n_chunks) - 1 - q : q) * TR;
             if constexpr (TMA) {
                 if (lane == 0) {
                     const uint32_t bar = smem_addr(&blk.full[n % S]);
@@ -386,7 +397,12 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
                 }
                 __syncwarp();
             }
-            fill_info(p, row0, info, lane);
+            fill_info<TR>(p, row0, info, lane);
+            if (lane == 0) {
+                info.row0 = row0;
+                info.strip = int(strip);
+                info.q = int(q);
+            }
         }
         if (lane == 0) info.tile = tile;
         __syncwarp();
@@ -396,29 +412,29 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
 }
 
 // A carry warp: tiles c, c + kCarryWarps, ... of the block.  Forward (DIR +1):
-// warps in order; the state entering each chunk is kept in p.states if given.
-// Backward (DIR -1): warps from the last, and beside them (map 1) the states
-// of the forward recurrence within the tile, from p.states.
-template <int E, int S, int Q, int DIR, class B>
+// warps in order; the states entering the tile and its second half are kept
+// in p.states if given.  Backward (DIR -1): warps from the last, and beside
+// them (map 1) the states of the forward recurrence within the tile, from
+// p.states.
+template <int E, int S, int TR, int DIR, class B>
 __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, int lane) {
     Waiter wait{p.status, kTileWait};
     for (int n = c;; n += kCarryWarps) {
         wait(&blk.full[n % S], n / S);
-        const TileInfo &info = blk.info[n % S];
-        const int64_t tile = info.tile;
-        if (tile >= p.n_tiles) return;
-        const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
-        const bool fresh = DIR > 0 ? info.start[0] >= 0 : info.end[kTR - 1] >= 0;
-        const int e0 = n % Q;
-        const int64_t d0 = int64_t(strip) * 32 * E + lane * E;
+        const TileInfo<TR> &info = blk.info[n % S];
+        if (info.tile >= p.n_tiles) return;
+        const int64_t q = info.q, strip = info.strip;
+        const bool fresh = DIR > 0 ? info.start[0] >= 0 : info.end[TR - 1] >= 0;
+        const int e0 = n % kQ;
+        const int64_t d0 = strip * 32 * E + lane * E;
         float hf[E];
         if constexpr (DIR < 0) {
-            const uint32_t chunk = uint32_t(p.n_chunks) - 1 - q;
+            const int64_t chunk = p.n_chunks - 1 - q;
             const bool begins = info.start[0] >= 0 || chunk == 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) hf[e] = begins || d0 + e >= p.D ? 0.f : p.states[int64_t(chunk) * p.D + d0 + e];
+            for (int e = 0; e < E; ++e) hf[e] = begins || d0 + e >= p.D ? 0.f : p.states[chunk * p.D + d0 + e];
         }
-        wait(&blk.maps[e0], n / Q);
+        wait(&blk.maps[e0], n / kQ);
         auto map_of = [&](int k, int w, int e) {
             return make_float2(reinterpret_cast<const float *>(&blk.A[k][e0][w][lane])[e],
                                reinterpret_cast<const float *>(&blk.B[k][e0][w][lane])[e]);
@@ -448,72 +464,96 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
         carry_tile_state<E>(p, strip, q, lane, fresh, tot, hin, [&] {
             if constexpr (DIR < 0) enter(1, true, hf);
         });
-        const float first[2] = {hin[0], hin[E - 1]};
+        float keep[2][E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) keep[0][e] = hin[e];
         enter(0, DIR > 0, hin);
+        if constexpr (DIR > 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                keep[1][e] = reinterpret_cast<const float *>(&blk.enter[0][e0][kWarps / 2][lane])[e];
+        }
         __syncwarp();
         if (lane == 0) arrive(&blk.in[e0]);
         if constexpr (DIR > 0) {
             if (p.states) {
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (d0 + e < p.D) p.states[q * p.D + d0 + e] = first[e];
+                for (int k = 0; k < 2; ++k) {
+                    if ((2 * q + k) * kBwdTR >= p.rows) continue;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (d0 + e < p.D) p.states[(2 * q + k) * p.D + d0 + e] = keep[k][e];
+                }
             }
         }
     }
 }
 
-// What a data warp knows of a tile: its place and, per row of the warp (bit
-// r), whether the row starts or ends a sequence and lies in one.
-struct WarpTile {
-    int64_t row0, d0;
-    uint32_t q, chunk;
-    uint32_t starts, ends, live;
-    int slot;
-    bool dvalid;
-};
-template <int TC>
-__device__ __forceinline__ WarpTile warp_tile(const GatedParams &p, const TileInfo &info, int slot, bool reverse, int warp,
-                                              int lane, int E) {
-    WarpTile t;
-    const uint32_t tile = uint32_t(info.tile);
-    t.slot = slot;
-    t.q = tile / uint32_t(p.n_strips);
-    t.chunk = reverse ? uint32_t(p.n_chunks) - 1 - t.q : t.q;
-    t.row0 = int64_t(t.chunk) * kTR + warp * kRows;
-    t.d0 = int64_t(tile - t.q * uint32_t(p.n_strips)) * TC + lane * E;
-    t.dvalid = t.d0 < p.D;
-    const int rr = lane & (kRows - 1);
-    constexpr uint32_t all = (1u << kRows) - 1u;
-    t.starts = __ballot_sync(0xffffffffu, info.start[warp * kRows + rr] >= 0) & all;
-    t.ends = __ballot_sync(0xffffffffu, info.end[warp * kRows + rr] >= 0) & all;
-    t.live = __ballot_sync(0xffffffffu, t.row0 + rr >= info.lo && t.row0 + rr < info.hi) & all;
-    return t;
-}
-
-// The thread's rows of operand OP of a tile: from the slot, or from memory
-// (read twice then, the second time from a cache).
-template <typename IO, int E, bool TMA, class Shape, int OP>
-__device__ __forceinline__ void tile_rows(const GatedParams &p, const unsigned char *smem, const WarpTile &t, int warp,
-                                          int lane, const void *base, int64_t rs, typename Raw<IO, E>::type (&x)[kRows]) {
-    using R = typename Raw<IO, E>::type;
-    if constexpr (TMA) {
-        const R *src = reinterpret_cast<const R *>(smem + t.slot * Shape::slot_bytes + OP * Shape::op_bytes) +
-                       warp * kRows * 32 + lane;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) x[r] = src[r * 32];
-    } else {
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const bool ok = t.dvalid && t.row0 + r < p.rows;
-            x[r] = ok ? *reinterpret_cast<const R *>(static_cast<const IO *>(base) + (t.row0 + r) * rs + t.d0) : R(0);
-        }
+// The thread's row r of an operand: from the slot, or from memory.
+template <typename IO, int E, bool TMA, int R>
+struct RowReader {
+    using Word = typename Raw<IO, E>::type;
+    const Word *src;                       // slot: the warp's first row
+    const char *base;                      // memory: the same
+    int64_t pitch;
+    int rows;                              // rows of the warp that exist, 0 past the last channel
+    __device__ __forceinline__ typename FVec<E>::type operator()(int r) const {
+        if constexpr (TMA) return Conv<IO, E>::in(src[r * 32]);
+        else return Conv<IO, E>::in(r < rows ? *reinterpret_cast<const Word *>(base + r * pitch) : Word(0));
     }
+};
+template <typename IO, int E, bool TMA, int R, class Shape, int OP>
+__device__ __forceinline__ RowReader<IO, E, TMA, R> reader(const GatedParams &p, const unsigned char *smem, int slot, int warp,
+                                                           int lane, int64_t row, int64_t d0, const void *base, int64_t rs) {
+    using Word = typename Raw<IO, E>::type;
+    RowReader<IO, E, TMA, R> x;
+    if constexpr (TMA) {
+        x.src = reinterpret_cast<const Word *>(smem + slot * Shape::slot_bytes + OP * Shape::op_bytes) + warp * R * 32 + lane;
+    } else {
+        const int64_t left = d0 < p.D ? p.rows - row : 0;
+        x.rows = int(left < 0 ? 0 : (left < R ? left : R));
+        x.base = static_cast<const char *>(base) + (row * rs + d0) * int64_t(sizeof(IO));
+        x.pitch = rs * int64_t(sizeof(IO));
+    }
+    return x;
 }
 
 // ------------------------------------------------------------- forward
+//
+// What a thread keeps of an element between fold and replay, and the step.
+// 16-bit I/O: a = sigmoid(f) = 1 / (1 + 2^(-f log2 e)) to about 2^-22 and
+// z = 1 - a, which is where fp32 itself ends for a near 1; half a step of a
+// 16-bit f moves z by 2^-12 |f| of itself or more, as much as 2^-22 does at
+// f = 8.  fp32 I/O: signed_small, either probability to its own precision.
+template <int GATE, typename IO, class V>
+__device__ __forceinline__ V fwd_gate(V f) {
+    if constexpr (GATE == GATE_LOG) {
+        return vmap(f, [](float x) { return log_decay<sizeof(IO) == 4>(x); });
+    } else if constexpr (sizeof(IO) == 4) {
+        return vmap(f, [](float x) { return signed_small(x); });
+    } else {
+        const V e = vmap(vmul(f, vset<V>(kNegLog2e)), [](float x) { return fast_exp2(x); });
+        return vmap(vadd(e, vset<V>(1.f)), [](float x) { return fast_rcp(x); });
+    }
+}
+template <int GATE, typename IO, class V>
+__device__ __forceinline__ void fwd_step(V g, V v, V &a, V &b) {
+    if constexpr (GATE == GATE_LOG) {
+        a = g;
+        b = v;
+    } else if constexpr (sizeof(IO) == 4) {
+        V z;
+        split_small(g, a, z);
+        b = vmul(z, v);
+    } else {
+        a = g;
+        b = vmul(vfma(g, vset<V>(-1.f), vset<V>(1.f)), v);
+    }
+}
+
 template <typename IO, int E, bool TMA> struct ForwardShape {
-    using Ring = SmemShape<IO, E, 2, kSlots, TMA>;
-    using Blk = Block<typename FVec<E>::type, kSlots, kLag + 1, 1>;
+    using Ring = SmemShape<IO, E, 2, kSlots, kTR, TMA>;
+    using Blk = Block<typename FVec<E>::type, kSlots, kTR, 1>;
     static constexpr uint32_t smem_bytes = Ring::ring_bytes + sizeof(Blk);
 };
 
@@ -521,92 +561,108 @@ template <typename IO, int E, int GATE, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
 gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_v) {
     using V = typename FVec<E>::type;
-    using R = typename Raw<IO, E>::type;
+    using W = typename Raw<IO, E>::type;
     using C = Conv<IO, E>;
     using Shape = typename ForwardShape<IO, E, TMA>::Ring;
     using Blk = typename ForwardShape<IO, E, TMA>::Blk;
-    constexpr int S = kSlots, Q = kLag + 1, TC = 32 * E;
+    constexpr int S = kSlots, R = kRows, TC = 32 * E;
     extern __shared__ __align__(128) unsigned char smem[];
     Blk &blk = *reinterpret_cast<Blk *>(smem + Shape::ring_bytes);
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    init_block<Blk, S, Q>(blk);
+    init_block<S>(blk);
     if (warp < kWarps) {
         Waiter wait{p.status, kTileWait};
-        int n_end = 1 << 30;                               // tiles of the block, once known
-        for (int n = 0; n < n_end + kLag; ++n) {
-            if (n < n_end) {
-                const bool got = wait(&blk.full[n % S], n / S);
-                const TileInfo &info = blk.info[n % S];
-                if (info.tile >= p.n_tiles) {
-                    n_end = n;
-                } else {
-                    const WarpTile t = warp_tile<TC>(p, info, n % S, false, warp, lane, E);
-                    R rf[kRows], rv[kRows];
-                    tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
-                    tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
-                    V A = vset<V>(1.f), B = vset<V>(0.f);
+        V gate[2][R];
+        // tile n: gates into registers, the warp's map to shared memory; false behind the last tile
+        auto fold = [&](int n, V (&g)[R]) {
+            const bool got = wait(&blk.full[n % S], n / S);
+            const TileInfo<kTR> &info = blk.info[n % S];
+            if (info.tile >= p.n_tiles) return false;
+            const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
+            const auto f = reader<IO, E, TMA, R, Shape, 0>(p, smem, n % S, warp, lane, row, d0, p.f, p.f_rs);
+            const auto v = reader<IO, E, TMA, R, Shape, 1>(p, smem, n % S, warp, lane, row, d0, p.v, p.v_rs);
+            const uint4 k = info.masks[warp];
+            V A = vset<V>(1.f), B = vset<V>(0.f);
+            if (k.x == 0u) {
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
-                        V a, b;
-                        gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a, b);
-                        if (t.starts >> r & 1u) {
-                            A = vset<V>(-0.f);
-                            B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
-                        }
-                        B = vfma(a, B, b);
-                        A = vmul(A, a);
+                for (int r = 0; r < R; ++r) {
+                    V a, b;
+                    g[r] = fwd_gate<GATE, IO>(f(r));
+                    fwd_step<GATE, IO>(g[r], v(r), a, b);
+                    B = vfma(a, B, b);
+                    A = vmul(A, a);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    V a, b;
+                    g[r] = fwd_gate<GATE, IO>(f(r));
+                    fwd_step<GATE, IO>(g[r], v(r), a, b);
+                    if (k.x >> r & 1u) {
+                        A = vset<V>(-0.f);
+                        B = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
                     }
-                    if (!got) A = B = vset<V>(__int_as_float(0x7fffffff));
-                    blk.A[0][n % Q][warp][lane] = A;
-                    blk.B[0][n % Q][warp][lane] = B;
-                    __syncwarp();
-                    if (lane == 0) arrive(&blk.maps[n % Q]);
+                    B = vfma(a, B, b);
+                    A = vmul(A, a);
                 }
             }
-            const int m = n - kLag;
-            if (m < 0 || m >= n_end) continue;
-            const bool got = wait(&blk.in[m % Q], m / Q);
-            const TileInfo &info = blk.info[m % S];
-            const WarpTile t = warp_tile<TC>(p, info, m % S, false, warp, lane, E);
-            R rf[kRows], rv[kRows];
-            tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
-            tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
-            V h = got ? blk.enter[0][m % Q][warp][lane] : vset<V>(__int_as_float(0x7fffffff));
-            char *dst = static_cast<char *>(p.h) + (t.row0 * p.h_rs + t.d0) * int64_t(sizeof(IO));
+            if (!got) A = B = vset<V>(nan_value());
+            blk.A[0][n % kQ][warp][lane] = A;
+            blk.B[0][n % kQ][warp][lane] = B;
+            __syncwarp();
+            if (lane == 0) arrive(&blk.maps[n % kQ]);
+            return true;
+        };
+        auto replay = [&](int n, const V (&g)[R]) {
+            const TileInfo<kTR> &info = blk.info[n % S];
+            const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
+            const auto v = reader<IO, E, TMA, R, Shape, 1>(p, smem, n % S, warp, lane, row, d0, p.v, p.v_rs);
+            const uint4 k = info.masks[warp];
+            const bool dvalid = d0 < p.D;
+            char *dst = static_cast<char *>(p.h) + (row * p.h_rs + d0) * int64_t(sizeof(IO));
             const int64_t pitch = p.h_rs * int64_t(sizeof(IO));
-            if (t.starts == 0u && t.ends == 0u && t.live == (1u << kRows) - 1u) {
+            const bool got = wait(&blk.in[n % kQ], n / kQ);
+            V h = got ? blk.enter[0][n % kQ][warp][lane] : vset<V>(nan_value());
+            if (k.w) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
+                for (int r = 0; r < R; ++r) {
                     V a, b;
-                    gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a, b);
+                    fwd_step<GATE, IO>(g[r], v(r), a, b);
                     h = vfma(a, h, b);
-                    if (t.dvalid) __stcs(reinterpret_cast<R *>(dst), C::out(h));
+                    if (dvalid) __stcs(reinterpret_cast<W *>(dst), C::out(h));
                     dst += pitch;
                 }
             } else {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
+                for (int r = 0; r < R; ++r) {
                     V a, b;
-                    gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a, b);
-                    if (t.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
+                    fwd_step<GATE, IO>(g[r], v(r), a, b);
+                    if (k.x >> r & 1u) h = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
                     h = vfma(a, h, b);
-                    if (t.dvalid && t.row0 + r < p.rows) {
-                        if (t.live >> r & 1u) __stcs(reinterpret_cast<R *>(dst), C::out(h));
-                        else if (p.zero_padding) __stcs(reinterpret_cast<R *>(dst), R(0));
+                    if (dvalid && row + r < p.rows) {
+                        if (k.z >> r & 1u) __stcs(reinterpret_cast<W *>(dst), C::out(h));
+                        else if (p.zero_padding) __stcs(reinterpret_cast<W *>(dst), W(0));
                     }
                     dst += pitch;
-                    if ((t.ends >> r & 1u) && p.h_last)
-                        put_state_row<E>(p.h_last, info.end[warp * kRows + r] * p.D, t.d0, p.D, h);
+                    if ((k.y >> r & 1u) && p.h_last) put_state_row<E>(p.h_last, info.end[warp * R + r] * p.D, d0, p.D, h);
                 }
             }
             __syncwarp();
-            if (lane == 0) arrive(&blk.empty[m % S]);
+            if (lane == 0) arrive(&blk.empty[n % S]);
+        };
+        for (int n = 0;; n += 2) {
+            const bool even = fold(n, gate[0]);
+            if (n > 0) replay(n - 1, gate[1]);
+            if (!even) break;
+            const bool odd = fold(n + 1, gate[1]);
+            replay(n, gate[0]);
+            if (!odd) break;
         }
     } else if (warp < kWarps + kCarryWarps) {
-        carry_loop<E, S, Q, 1>(p, blk, warp - kWarps, lane);
+        carry_loop<E, S, kTR, 1>(p, blk, warp - kWarps, lane);
     } else {
-        feed<S, 2, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, false, &map_f, &map_v, nullptr);
+        feed<S, 2, kTR, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, false, &map_f, &map_v, nullptr);
     }
     __syncthreads();
     empty_sequences(p, p.h_last, p.h0, p.h0_ss);
@@ -621,9 +677,9 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
 //   GATE_LOG:     dv = g,   df = [f <= 0] a h_{t-1} g
 // and dh0 of a sequence is r at its first row.  h_{t-1} is recomputed from
 // the fp32 state that entered the tile, saved by the forward pass (one row of
-// D per kTR rows), instead of being read back: the outputs h are not needed,
-// so the pass reads three arrays and not four, and the states have not been
-// rounded to 16 bits.
+// D per kBwdTR rows), instead of being read back: the outputs h are not
+// needed, so the pass reads three arrays and not four, and the states have
+// not been rounded to 16 bits.
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ V bwd_gate(V f) {
     // GATE_SIGMOID: signed small probability; GATE_LOG: a, negated where f > 0, which has no gradient
@@ -646,8 +702,8 @@ __device__ __forceinline__ void bwd_split(V s, V &a, V &z) {
 }
 
 template <typename IO, int E, bool TMA> struct BackwardShape {
-    using Ring = SmemShape<IO, E, 3, kBwdSlots, TMA>;
-    using Blk = Block<typename FVec<E>::type, kBwdSlots, kBwdLag + 1, 2>;       // maps 0: reverse, 1: forward
+    using Ring = SmemShape<IO, E, 3, kBwdSlots, kBwdTR, TMA>;
+    using Blk = Block<typename FVec<E>::type, kBwdSlots, kBwdTR, 2>;            // maps 0: reverse, 1: forward
     static constexpr uint32_t smem_bytes = Ring::ring_bytes + sizeof(Blk);
 };
 
@@ -656,117 +712,136 @@ __global__ void __launch_bounds__(kThreads, 1)
 gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f,
                            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dh) {
     using V = typename FVec<E>::type;
-    using R = typename Raw<IO, E>::type;
+    using W = typename Raw<IO, E>::type;
     using C = Conv<IO, E>;
     using Shape = typename BackwardShape<IO, E, TMA>::Ring;
     using Blk = typename BackwardShape<IO, E, TMA>::Blk;
-    constexpr int S = kBwdSlots, Q = kBwdLag + 1, TC = 32 * E;
+    constexpr int S = kBwdSlots, R = kBwdRows, TC = 32 * E;
     extern __shared__ __align__(128) unsigned char smem[];
     Blk &blk = *reinterpret_cast<Blk *>(smem + Shape::ring_bytes);
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    init_block<Blk, S, Q>(blk);
+    init_block<S>(blk);
     if (warp < kWarps) {
         Waiter wait{p.status, kTileWait};
-        int n_end = 1 << 30;
-        for (int n = 0; n < n_end + kBwdLag; ++n) {
-            if (n < n_end) {
-                const bool got = wait(&blk.full[n % S], n / S);
-                const TileInfo &info = blk.info[n % S];
-                if (info.tile >= p.n_tiles) {
-                    n_end = n;
-                } else {
-                    const WarpTile t = warp_tile<TC>(p, info, n % S, true, warp, lane, E);
-                    R rf[kRows], rv[kRows], rg[kRows];
-                    tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
-                    tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
-                    tile_rows<IO, E, TMA, Shape, 2>(p, smem, t, warp, lane, p.dh, p.dh_rs, rg);
-                    V a[kRows];
-                    V A = vset<V>(1.f), B = vset<V>(0.f);
+        V gate[2][R];
+        auto fold = [&](int n, V (&s)[R]) {
+            const bool got = wait(&blk.full[n % S], n / S);
+            const TileInfo<kBwdTR> &info = blk.info[n % S];
+            if (info.tile >= p.n_tiles) return false;
+            const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
+            const auto f = reader<IO, E, TMA, R, Shape, 0>(p, smem, n % S, warp, lane, row, d0, p.f, p.f_rs);
+            const auto v = reader<IO, E, TMA, R, Shape, 1>(p, smem, n % S, warp, lane, row, d0, p.v, p.v_rs);
+            const auto dh = reader<IO, E, TMA, R, Shape, 2>(p, smem, n % S, warp, lane, row, d0, p.dh, p.dh_rs);
+            const uint4 k = info.masks[warp];
+            V a[R];
+            V A = vset<V>(1.f), B = vset<V>(0.f);
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
-                        V b;
-                        gate_pair<GATE, IO>(C::in(rf[r]), C::in(rv[r]), a[r], b);
-                        if (t.starts >> r & 1u) {
-                            A = vset<V>(-0.f);
-                            B = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
-                        }
-                        B = vfma(a[r], B, b);
-                        A = vmul(A, a[r]);
-                    }
-                    V RA = vset<V>(1.f), RB = vset<V>(0.f);
-#pragma unroll
-                    for (int r = kRows - 1; r >= 0; --r) {
-                        if (t.ends >> r & 1u) {
-                            RA = vset<V>(-0.f);
-                            RB = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, t.d0, p.D);
-                        }
-                        RB = vmul(a[r], vadd(RB, C::in(rg[r])));
-                        RA = vmul(RA, a[r]);
-                    }
-                    if (!got) A = B = RA = RB = vset<V>(__int_as_float(0x7fffffff));
-                    blk.A[0][n % Q][warp][lane] = RA;
-                    blk.B[0][n % Q][warp][lane] = RB;
-                    blk.A[1][n % Q][warp][lane] = A;
-                    blk.B[1][n % Q][warp][lane] = B;
-                    __syncwarp();
-                    if (lane == 0) arrive(&blk.maps[n % Q]);
+            for (int r = 0; r < R; ++r) {
+                V z;
+                s[r] = bwd_gate<GATE, IO>(f(r));
+                bwd_split<GATE>(s[r], a[r], z);
+                if (k.x >> r & 1u) {
+                    A = vset<V>(-0.f);
+                    B = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
                 }
+                B = vfma(a[r], B, GATE == GATE_SIGMOID ? vmul(z, v(r)) : v(r));
+                A = vmul(A, a[r]);
             }
-            const int m = n - kBwdLag;
-            if (m < 0 || m >= n_end) continue;
-            const TileInfo &info = blk.info[m % S];
-            const WarpTile t = warp_tile<TC>(p, info, m % S, true, warp, lane, E);
-            R rv[kRows], rg[kRows];
-            V s[kRows], c[kRows];                                     // df = c g
-            {
-                R rf[kRows];
-                tile_rows<IO, E, TMA, Shape, 0>(p, smem, t, warp, lane, p.f, p.f_rs, rf);
+            V RA = vset<V>(1.f), RB = vset<V>(0.f);
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) s[r] = bwd_gate<GATE, IO>(C::in(rf[r]));
+            for (int r = R - 1; r >= 0; --r) {
+                if (k.y >> r & 1u) {
+                    RA = vset<V>(-0.f);
+                    RB = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
+                }
+                RB = vmul(a[r], vadd(RB, dh(r)));
+                RA = vmul(RA, a[r]);
             }
-            tile_rows<IO, E, TMA, Shape, 1>(p, smem, t, warp, lane, p.v, p.v_rs, rv);
-            const bool got = wait(&blk.in[m % Q], m / Q);
-            V h = blk.enter[1][m % Q][warp][lane];
+            if (!got) A = B = RA = RB = vset<V>(nan_value());
+            blk.A[0][n % kQ][warp][lane] = RA;
+            blk.B[0][n % kQ][warp][lane] = RB;
+            blk.A[1][n % kQ][warp][lane] = A;
+            blk.B[1][n % kQ][warp][lane] = B;
+            __syncwarp();
+            if (lane == 0) arrive(&blk.maps[n % kQ]);
+            return true;
+        };
+        auto replay = [&](int n, const V (&s)[R]) {
+            const TileInfo<kBwdTR> &info = blk.info[n % S];
+            const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
+            const auto v = reader<IO, E, TMA, R, Shape, 1>(p, smem, n % S, warp, lane, row, d0, p.v, p.v_rs);
+            const auto dh = reader<IO, E, TMA, R, Shape, 2>(p, smem, n % S, warp, lane, row, d0, p.dh, p.dh_rs);
+            const uint4 k = info.masks[warp];
+            const bool dvalid = d0 < p.D;
+            const bool got = wait(&blk.in[n % kQ], n / kQ);
+            V h = blk.enter[1][n % kQ][warp][lane];
+            V c[R];                                                   // df = c g
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (t.starts >> r & 1u) h = state_row<E>(p.h0, info.start[warp * kRows + r] * p.h0_ss, t.d0, p.D);
-                const V v = C::in(rv[r]);
+            for (int r = 0; r < R; ++r) {
+                if (k.x >> r & 1u) h = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
+                const V x = v(r);
                 V a, z;
                 bwd_split<GATE>(s[r], a, z);
                 if constexpr (GATE == GATE_SIGMOID) {
-                    c[r] = vmul(vmul(a, z), vfma(v, vset<V>(-1.f), h));
-                    h = vfma(a, h, vmul(z, v));
+                    c[r] = vmul(vmul(a, z), vfma(x, vset<V>(-1.f), h));
+                    h = vfma(a, h, vmul(z, x));
                 } else {
-                    c[r] = vmap(s[r], h, [](float x, float y) { return is_cut(x) ? 0.f : x * y; });
-                    h = vfma(a, h, v);
+                    c[r] = vmap(s[r], h, [](float y, float w) { return is_cut(y) ? 0.f : y * w; });
+                    h = vfma(a, h, x);
                 }
             }
-            tile_rows<IO, E, TMA, Shape, 2>(p, smem, t, warp, lane, p.dh, p.dh_rs, rg);
-            V flow = got ? blk.enter[0][m % Q][warp][lane] : vset<V>(__int_as_float(0x7fffffff));
+            V flow = got ? blk.enter[0][n % kQ][warp][lane] : vset<V>(nan_value());
+            char *pf = static_cast<char *>(p.df) + ((row + R - 1) * p.df_rs + d0) * int64_t(sizeof(IO));
+            char *pv = static_cast<char *>(p.dv) + ((row + R - 1) * p.dv_rs + d0) * int64_t(sizeof(IO));
+            const int64_t pitch_f = p.df_rs * int64_t(sizeof(IO)), pitch_v = p.dv_rs * int64_t(sizeof(IO));
+            if (k.w) {
 #pragma unroll
-            for (int r = kRows - 1; r >= 0; --r) {
-                if (t.ends >> r & 1u) flow = state_row<E>(p.dh_last, info.end[warp * kRows + r] * p.D, t.d0, p.D);
-                const V g = vadd(flow, C::in(rg[r]));
-                V a, z;
-                bwd_split<GATE>(s[r], a, z);
-                if (t.dvalid && t.row0 + r < p.rows) {
-                    const bool live = t.live >> r & 1u;
-                    store_raw<IO, E>(p.df, (t.row0 + r) * p.df_rs + t.d0, live ? C::out(vmul(c[r], g)) : R(0));
-                    store_raw<IO, E>(p.dv, (t.row0 + r) * p.dv_rs + t.d0,
-                                     live ? C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g) : R(0));
+                for (int r = R - 1; r >= 0; --r) {
+                    const V g = vadd(flow, dh(r));
+                    V a, z;
+                    bwd_split<GATE>(s[r], a, z);
+                    if (dvalid) {
+                        __stcs(reinterpret_cast<W *>(pf), C::out(vmul(c[r], g)));
+                        __stcs(reinterpret_cast<W *>(pv), C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g));
+                    }
+                    pf -= pitch_f;
+                    pv -= pitch_v;
+                    flow = vmul(a, g);
                 }
-                flow = vmul(a, g);
-                if ((t.starts >> r & 1u) && p.dh0)
-                    put_state_row<E>(p.dh0, info.start[warp * kRows + r] * p.D, t.d0, p.D, flow);
+            } else {
+#pragma unroll
+                for (int r = R - 1; r >= 0; --r) {
+                    if (k.y >> r & 1u) flow = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
+                    const V g = vadd(flow, dh(r));
+                    V a, z;
+                    bwd_split<GATE>(s[r], a, z);
+                    if (dvalid && row + r < p.rows) {
+                        const bool live = k.z >> r & 1u;
+                        __stcs(reinterpret_cast<W *>(pf), live ? C::out(vmul(c[r], g)) : W(0));
+                        __stcs(reinterpret_cast<W *>(pv), live ? C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g) : W(0));
+                    }
+                    pf -= pitch_f;
+                    pv -= pitch_v;
+                    flow = vmul(a, g);
+                    if ((k.x >> r & 1u) && p.dh0) put_state_row<E>(p.dh0, info.start[warp * R + r] * p.D, d0, p.D, flow);
+                }
             }
             __syncwarp();
-            if (lane == 0) arrive(&blk.empty[m % S]);
+            if (lane == 0) arrive(&blk.empty[n % S]);
+        };
+        for (int n = 0;; n += 2) {
+            const bool even = fold(n, gate[0]);
+            if (n > 0) replay(n - 1, gate[1]);
+            if (!even) break;
+            const bool odd = fold(n + 1, gate[1]);
+            replay(n, gate[0]);
+            if (!odd) break;
         }
     } else if (warp < kWarps + kCarryWarps) {
-        carry_loop<E, S, Q, -1>(p, blk, warp - kWarps, lane);
+        carry_loop<E, S, kBwdTR, -1>(p, blk, warp - kWarps, lane);
     } else {
-        feed<S, 3, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, true, &map_f, &map_v, &map_dh);
+        feed<S, 3, kBwdTR, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, true, &map_f, &map_v, &map_dh);
     }
     __syncthreads();
     empty_sequences(p, p.dh0, p.dh_last, p.D);

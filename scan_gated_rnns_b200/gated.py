@@ -173,7 +173,7 @@ def gated_scan_backward(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Ten
 
 class GatedScan(torch.autograd.Function):
     """The states that enter each chunk are kept for the backward pass (one
-    float32 row per 104 rows); the outputs are not."""
+    float32 row per 96 rows); the outputs are not."""
 
     @staticmethod
     def forward(ctx, f, v, h0, cu_seqlens, gate):

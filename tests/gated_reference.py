@@ -10,7 +10,10 @@ rounding is |f| 2^-24 in the exponent):
   sigmoid: both a and 1 - a to (2^-21 + |f| 2^-23) min(a, 1 - a), and a
            rounding 2^-24 of the larger one;
   log:     a to 2^-23 a where f > -1/4 (series), else (2^-21 + |f| 2^-23) a;
-  16-bit I/O: 2^-21 + |f| 2^-23 everywhere.
+  16-bit I/O, log: 2^-21 + |f| 2^-23 everywhere.
+  16-bit I/O, sigmoid: a = 1 / (1 + 2^x), the sum rounded (2^-24) and the
+           reciprocal off by 2^-23, so 2^-22 a on top of the above, and 1 - a
+           is off by as much and its own rounding, 2^-24.
 The hardware's 2^x gives 0 for results below 2^-126, the smallest normal
 number, so a probability or decay is off by at most 2^-126 there whatever its
 relative error: that much is added to each.
@@ -33,6 +36,9 @@ def gate64(f, v, gate, precise):
             a, z = np.where(f >= 0, big, small), np.where(f >= 0, small, big)
             err = np.where(small == 0, 0.0, rel * small + 2.0 ** -126)
             a, z = np.where(np.isnan(f), np.nan, a), np.where(np.isnan(f), np.nan, z)
+            if not precise:
+                err = err + 2.0 ** -22 * a
+                return a, z * v, z, err, (err + 2.0 ** -24 + 2.0 ** -23 * z) * np.abs(v)
             return a, z * v, z, err + 2.0 ** -24 * a, (err + 2.0 ** -23 * z) * np.abs(v)
         x = np.where(f > 0, 0.0, f)
         a = np.exp(x)
