@@ -80,9 +80,20 @@ struct GatedParams {
     uint32_t spin_limit;
 };
 
-__device__ __forceinline__ int64_t cu_at(const GatedParams &p, int64_t i) {
-    return p.cu_bytes == 8 ? static_cast<const int64_t *>(p.cu)[i] : int64_t(static_cast<const int32_t *>(p.cu)[i]);
+// bound i, clamped to what rows can be
+__device__ __forceinline__ int cu_at(const GatedParams &p, int64_t i) {
+    const int64_t b = p.cu_bytes == 8 ? static_cast<const int64_t *>(p.cu)[i] : int64_t(static_cast<const int32_t *>(p.cu)[i]);
+    return int(b < -1 ? -1 : (b > p.rows + 1 ? p.rows + 1 : b));
 }
+// The bounds as the feeding warp reads them: from shared memory, where they
+// are copied once if they fit (every tile looks them up, and a chain of loads
+// from L2 took longer than the tile).
+constexpr int kBoundsHeld = 1024;
+struct Bounds {
+    const GatedParams &p;
+    const int *held;                       // or null
+    __device__ __forceinline__ int operator()(int64_t i) const { return held ? held[i] : cu_at(p, i); }
+};
 
 __device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) >> 31; }
 // the map (A, B) applied to a state, and `then` after `first`
@@ -95,6 +106,7 @@ __device__ __forceinline__ float2 then_map(float2 first, float2 then) {
 template <int TR> struct TileInfo {
     int64_t tile, row0;                    // tile n_tiles: no more
     int strip, q;                          // its strip, and its place along it in processing order
+    int cut;                               // a sequence starts (1) or ends (2) in the tile
     uint4 masks[kWarps];                   // of each data warp's rows: starts, ends, in a sequence; .w: all plain
     int start[TR], end[TR];                // sequence that starts (ends) at the row, or -1
 };
@@ -103,7 +115,7 @@ template <int TR> struct TileInfo {
 // that are not ascending give wrong sequences but never a row or a sequence
 // outside the buffers.
 template <int TR>
-__device__ __forceinline__ void fill_info(const GatedParams &p, int64_t row0, TileInfo<TR> &t, int lane) {
+__device__ __forceinline__ void fill_info(const GatedParams &p, const Bounds &cu, int64_t row0, TileInfo<TR> &t, int lane) {
     constexpr int R = TR / kWarps;
     const int64_t row_end = row0 + TR < p.rows ? row0 + TR : p.rows;
     int64_t lo_row = 0, hi_row = p.rows;   // rows that lie in sequences
@@ -122,27 +134,27 @@ __device__ __forceinline__ void fill_info(const GatedParams &p, int64_t row0, Ti
         }
     } else {
         for (int r = lane; r < TR; r += 32) t.start[r] = t.end[r] = -1;
-        lo_row = cu_at(p, 0);
-        const int64_t last = cu_at(p, p.n_seqs);
+        lo_row = cu(0);
+        const int64_t last = cu(p.n_seqs);
         hi_row = last < p.rows ? last : p.rows;
         // bounds at or below row0, by a 33-way search: the last of them begins the
         // sequence that holds row0
-        int64_t lo = 0, hi = p.n_seqs + 1;
+        int lo = 0, hi = int(p.n_seqs) + 1;
         while (lo < hi) {
-            const int64_t step = (hi - lo + 31) / 32;
-            const int64_t i = lo + (lane + 1) * step - 1;
-            const bool below = i < hi && cu_at(p, i) <= row0;
+            const int step = (hi - lo + 31) / 32;
+            const int64_t i = int64_t(lo) + int64_t(lane + 1) * step - 1;
+            const bool below = i < hi && cu(i) <= row0;
             const int n = __popc(__ballot_sync(0xffffffffu, below));
-            const int64_t next = lo + n * step;
-            const int64_t top = lo + (n + 1) * step - 1;
-            lo = next < hi ? next : hi;
-            hi = top < hi ? top : hi;
+            const int64_t next = int64_t(lo) + int64_t(n) * step;
+            const int64_t top = int64_t(lo) + int64_t(n + 1) * step - 1;
+            lo = int(next < hi ? next : hi);
+            hi = int(top < hi ? top : hi);
         }
         __syncwarp();
         for (int64_t s = (lo > 0 ? lo - 1 : 0) + lane;; s += 32) {
             bool more = false;
             if (s < p.n_seqs) {
-                const int64_t b = cu_at(p, s), e = cu_at(p, s + 1);
+                const int64_t b = cu(s), e = cu(s + 1);
                 more = b < row_end;
                 if (b < e) {
                     if (b >= row0 && b < row_end) t.start[b - row0] = int(s);
@@ -153,18 +165,21 @@ __device__ __forceinline__ void fill_info(const GatedParams &p, int64_t row0, Ti
         }
     }
     __syncwarp();
+    int cut = 0;
 #pragma unroll
     for (int r0 = 0; r0 < TR; r0 += 32) {
         const int r = r0 + lane;
         const uint32_t starts = __ballot_sync(0xffffffffu, r < TR && t.start[r < TR ? r : 0] >= 0);
         const uint32_t ends = __ballot_sync(0xffffffffu, r < TR && t.end[r < TR ? r : 0] >= 0);
         const uint32_t live = __ballot_sync(0xffffffffu, r < TR && row0 + r >= lo_row && row0 + r < hi_row);
+        cut |= (starts ? 1 : 0) | (ends ? 2 : 0);
         if (lane < 32 / R && r0 / R + lane < kWarps) {
             constexpr uint32_t all = (1u << R) - 1u;
             const uint32_t a = starts >> (lane * R) & all, b = ends >> (lane * R) & all, c = live >> (lane * R) & all;
             t.masks[r0 / R + lane] = make_uint4(a, b, c, a == 0u && b == 0u && c == all);
         }
     }
+    if (lane == 0) t.cut = cut;
 }
 
 __device__ __forceinline__ uint32_t ld_relaxed_u32(const uint32_t *p) {
@@ -179,29 +194,56 @@ __device__ __forceinline__ uint64_t pack_map(float2 m) {
     return (uint64_t(__float_as_uint(m.y)) << 32) | __float_as_uint(m.x);
 }
 
+// The words of this lane's E channels: each is read whole.
+template <int E> __device__ __forceinline__ void load_maps(const uint64_t *p, uint64_t (&m)[E]) {
+    if constexpr (E == 1) {
+        m[0] = ld_relaxed_u64(p);
+    } else {
+        asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(m[0]), "=l"(m[1]) : "l"(p) : "memory");
+    }
+}
+template <int E> __device__ __forceinline__ void load_states(const uint32_t *p, uint32_t (&s)[E]) {
+    if constexpr (E == 1) {
+        s[0] = ld_relaxed_u32(p);
+    } else {
+        asm volatile("ld.relaxed.gpu.global.v2.u32 {%0, %1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "l"(p) : "memory");
+    }
+}
+template <int E> __device__ __forceinline__ bool words_in(const uint64_t (&m)[E]) {
+    bool ok = m[0] != ~uint64_t(0);
+    if constexpr (E == 2) ok = ok && m[1] != ~uint64_t(0);
+    return ok;
+}
+template <int E> __device__ __forceinline__ bool words_in(const uint32_t (&s)[E]) {
+    bool ok = s[0] != kNone;
+    if constexpr (E == 2) ok = ok && s[1] != kNone;
+    return ok;
+}
+template <int E> __device__ __forceinline__ void apply_words(const uint64_t (&m)[E], float (&h)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        h[e] = apply_map(__uint_as_float(uint32_t(m[e])), __uint_as_float(uint32_t(m[e] >> 32)), h[e]);
+}
+
 // The carry of one tile (carry warp): q its place in processing order along
 // its strip, tot the tile's maps of this lane's E channels.  Publishes,
 // waits, and returns the entering states.  Tiles whose first row (in
-// processing order) is a start enter with 0, which they never use.  The
-// window holds the words of the W tiles before: all are read in one round
-// trip, and again only those not yet published.  W tiles are what one hop of
-// the chain advances (about 1 us); 16 (8 with two channels a lane) fit the
-// registers.
-// `between` runs once the tile's own words are out.
-template <int E, class Between>
+// processing order) is a start enter with 0, which they never use.  One round
+// trip reads the words of the kNear tiles before for every channel, and those
+// of 32 more for the strip's first channel: as a rule the state is among the
+// near ones (wide rows: few tiles of a strip are in flight), else a second
+// round trip reads the rest of the channels.  `meanwhile` runs under the
+// first.
+constexpr int kNear = 4;
+template <int E, class Meanwhile>
 __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int64_t q, int lane, bool fresh,
-                                                 const float2 (&tot)[E], float (&hin)[E], Between between) {
+                                                 bool cut, const float2 (&tot)[E], float (&hin)[E], Meanwhile meanwhile) {
     constexpr int TC = 32 * E;
-    constexpr int W = E == 1 ? 16 : 8;
     const int64_t step = p.n_strips * TC;                          // from a tile's words to the next chunk's
     const int64_t at = q * step + strip * TC + lane * E;
     const bool last = q + 1 == p.n_chunks;
-    bool cut = true;                                               // a start cuts all channels alike
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        hin[e] = 0.f;
-        cut = cut && is_cut(tot[e].x);
-    }
+    for (int e = 0; e < E; ++e) hin[e] = 0.f;
     auto publish_state = [&] {
         if (last) return;
 #pragma unroll
@@ -209,65 +251,97 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
     };
     if (fresh || q == 0) {
         publish_state();
-        between();
+        meanwhile();
         return;
     }
-    if (cut) {
+    if (cut) {                                                     // a start within: the state does not depend on what enters
         publish_state();
     } else if (!last) {
 #pragma unroll
         for (int e = 0; e < E; ++e) st_relaxed_u64(p.maps + at + e, pack_map(tot[e]));
     }
-    between();
-    uint64_t m[W][E];
-    uint32_t st[W][E];
+    bool found = false;
+    for (uint32_t polls = 0; !found; ++polls) {
+        uint64_t m[kNear][E];
+        uint32_t st[kNear][E];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            m[i][e] = ~uint64_t(0);
-            st[i][e] = kNone;
-        }
-    }
-    int k = -1;                                                    // nearest published state, maps there before it
-    for (uint32_t polls = 0;; ++polls) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (q - 1 - i < 0) continue;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (st[i][e] == kNone) st[i][e] = ld_relaxed_u32(p.carry + at + e - (i + 1) * step);
-                if (i < W - 1 && m[i][e] == ~uint64_t(0)) m[i][e] = ld_relaxed_u64(p.maps + at + e - (i + 1) * step);
+        for (int i = 0; i < kNear; ++i) {
+            if (q - 1 - i >= 0) {
+                load_states<E>(p.carry + at - (i + 1) * step, st[i]);
+                load_maps<E>(p.maps + at - (i + 1) * step, m[i]);
+            } else {
+                st[i][0] = kNone;
+                m[i][0] = ~uint64_t(0);
             }
         }
+        const int64_t far = q - 1 - kNear - lane;                  // the tile that this lane probes
+        uint32_t ps = kNone;
+        uint64_t pm = ~uint64_t(0);
+        if (far >= 0) {
+            ps = ld_relaxed_u32(p.carry + far * step + strip * TC);
+            pm = ld_relaxed_u64(p.maps + far * step + strip * TC);
+        }
+        if (polls == 0) meanwhile();
+        int k = -1;                                                // nearest published state, maps there before it
         bool there = true;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            bool s_ok = true, m_ok = true;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                s_ok = s_ok && st[i][e] != kNone;
-                m_ok = m_ok && m[i][e] != ~uint64_t(0);
-            }
-            if (there && k < 0 && s_ok) k = i;
-            there = there && m_ok;
+        for (int i = 0; i < kNear; ++i) {
+            if (there && k < 0 && words_in<E>(st[i])) k = i;
+            there = there && words_in<E>(m[i]);
         }
-        if (__all_sync(0xffffffffu, k >= 0) || polls >= p.spin_limit) break;
-        if (polls > 8) __nanosleep(32);
-    }
-    if (k < 0) {
-        atomicExch(p.status, 5u);                                  // SGR_ERR_TIMEOUT
+        if (__all_sync(0xffffffffu, k >= 0)) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) hin[e] = __int_as_float(0x7fffffff);
-    } else {
+            for (int i = kNear - 1; i >= 0; --i) {
+                if (i == k) {
 #pragma unroll
-        for (int i = W - 1; i >= 0; --i) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (i == k) hin[e] = __uint_as_float(st[i][e]);
-                else if (i < k)
-                    hin[e] = apply_map(__uint_as_float(uint32_t(m[i][e])), __uint_as_float(uint32_t(m[i][e] >> 32)), hin[e]);
+                    for (int e = 0; e < E; ++e) hin[e] = __uint_as_float(st[i][e]);
+                } else if (i < k) {
+                    apply_words<E>(m[i], hin);
+                }
             }
+            found = true;
+        } else if (__all_sync(0xffffffffu, there)) {
+            const uint32_t has_state = __ballot_sync(0xffffffffu, ps != kNone);
+            const uint32_t has_map = __ballot_sync(0xffffffffu, pm != ~uint64_t(0));
+            const int j = has_state ? __ffs(has_state) - 1 : 0;
+            const uint32_t nearer = (1u << j) - 1u;
+            if (has_state && (has_map & nearer) == nearer) {
+                uint32_t s0[E];
+                load_states<E>(p.carry + at - (kNear + j + 1) * step, s0);
+                bool ok = true;
+                for (int i0 = j; i0 > 0; i0 -= 4) {                // maps of the far tiles, oldest first
+                    uint64_t w[4][E];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i0 - u > 0) load_maps<E>(p.maps + at - (kNear + i0 - u) * step, w[u]);
+                    if (i0 == j) {
+                        ok = words_in<E>(s0);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) hin[e] = __uint_as_float(s0[e]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (i0 - u > 0) {
+                            ok = ok && words_in<E>(w[u]);
+                            apply_words<E>(w[u], hin);
+                        }
+                    }
+                }
+                if (j == 0) {
+                    ok = words_in<E>(s0);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) hin[e] = __uint_as_float(s0[e]);
+                }
+#pragma unroll
+                for (int i = kNear - 1; i >= 0; --i) apply_words<E>(m[i], hin);
+                found = __all_sync(0xffffffffu, ok);
+            }
+        }
+        if (!found && polls >= p.spin_limit) {
+            if (lane == 0) atomicExch(p.status, 5u);               // SGR_ERR_TIMEOUT
+#pragma unroll
+            for (int e = 0; e < E; ++e) hin[e] = __int_as_float(0x7fffffff);
+            found = true;
         }
     }
     if (!cut) publish_state();
@@ -316,8 +390,12 @@ template <typename V, int S, int TR, int MAPS> struct Block {
     uint64_t full[S], empty[S];            // copies and table there; replayed by every data warp
     uint64_t maps[kQ], in[kQ];             // maps there; entering states there
     TileInfo<TR> info[S];
+    // maps of the data warps, then (by the carry warp) of everything before
+    // each of them in the tile; the forward maps of a backward tile (1) turn
+    // into the states entering each warp, in A
     V A[MAPS][kQ][kWarps][32], B[MAPS][kQ][kWarps][32];
-    V enter[MAPS][kQ][kWarps][32];
+    V enter[kQ][32];                       // states entering the tile
+    int bounds[kBoundsHeld];
 };
 template <int S, class B> __device__ __forceinline__ void init_block(B &blk) {
     if (threadIdx.x == 0) {
@@ -366,25 +444,29 @@ template <int S, int OPS, int TR, uint32_t OP_BYTES, int TC, bool TMA, class B>
 __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slots, int lane, bool reverse,
                                      const CUtensorMap *m0, const CUtensorMap *m1, const CUtensorMap *m2) {
     Waiter wait{p.status, kTileWait};
+    // the next ticket is drawn a tile ahead, so that its round trip passes under the work on this one
+    uint32_t ticket = 0;
+    if (p.ticket) {
+        if (lane == 0) ticket = atomicAdd(p.ticket, 1u) + 1u;
+    } else {
+        ticket = blockIdx.x;
+    }
+    const bool held = p.cu != nullptr && p.n_seqs < kBoundsHeld;
+    if (held)
+        for (int i = lane; i <= int(p.n_seqs); i += 32) blk.bounds[i] = cu_at(p, i);
+    const Bounds bounds{p, held ? blk.bounds : nullptr};
+    __syncwarp();
     int ends = 0;
     for (int n = 0; ends < kCarryWarps; ++n) {
-        int64_t tile = p.n_tiles;
-        if (ends > 0) {
-        } else if (p.ticket) {
-            uint32_t t = 0;
-            if (lane == 0) t = atomicAdd(p.ticket, 1u) + 1u;
-            tile = __shfl_sync(0xffffffffu, t, 0);
-        } else if (n == 0) {
-            tile = blockIdx.x;
-        }
-        const bool more = tile < p.n_tiles;
+        const uint32_t tile = __shfl_sync(0xffffffffu, ticket, 0);
+        const bool more = ends == 0 && tile < uint32_t(p.n_tiles);
         if (n >= S) wait(&blk.empty[n % S], n / S - 1);
         TileInfo<TR> &info = blk.info[n % S];
         if (more) {
-            const uint32_t q = uint32_t(tile) / uint32_t(p.n_strips), strip = uint32_t(tile) - q * uint32_t(p.n_strips);
+            const uint32_t q = tile / uint32_t(p.n_strips), strip = tile - q * uint32_t(p.n_strips);
             const int64_t row0 = int64_t(reverse ? uint32_t(p.n_chunks) - 1 - q : q) * TR;
-            if constexpr (TMA) {
-                if (lane == 0) {
+            if (lane == 0) {
+                if constexpr (TMA) {
                     const uint32_t bar = smem_addr(&blk.full[n % S]);
                     const uint32_t dst = slots + uint32_t(n % S) * (OPS * OP_BYTES);
                     // the data warps' reads of the slot came before the copies into it
@@ -395,29 +477,55 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
                     tma_load_2d(dst + OP_BYTES, m1, int(strip) * TC, int(row0), bar);
                     if constexpr (OPS == 3) tma_load_2d(dst + 2 * OP_BYTES, m2, int(strip) * TC, int(row0), bar);
                 }
-                __syncwarp();
-            }
-            fill_info<TR>(p, row0, info, lane);
-            if (lane == 0) {
+                ticket = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : uint32_t(p.n_tiles);
                 info.row0 = row0;
                 info.strip = int(strip);
                 info.q = int(q);
             }
+            __syncwarp();
+            fill_info<TR>(p, bounds, row0, info, lane);
+        } else {
+            ++ends;
         }
-        if (lane == 0) info.tile = tile;
+        if (lane == 0) info.tile = more ? int64_t(tile) : p.n_tiles;
         __syncwarp();
         if (lane == 0) arrive(&blk.full[n % S]);
-        if (!more) ++ends;
     }
 }
 
-// A carry warp: tiles c, c + kCarryWarps, ... of the block.  Forward (DIR +1):
-// warps in order; the states entering the tile and its second half are kept
-// in p.states if given.  Backward (DIR -1): warps from the last, and beside
-// them (map 1) the states of the forward recurrence within the tile, from
-// p.states.
+// Maps of a channel's E elements composed: `then` after `first`.
+template <class V> __device__ __forceinline__ void compose(V &A, V &B, V a, V b, bool cuts) {
+    if (cuts) {
+        if constexpr (sizeof(V) == 4) {
+            const float2 m = then_map(make_float2(A, B), make_float2(a, b));
+            A = m.x;
+            B = m.y;
+        } else {
+            const float2 x = then_map(make_float2(A.x, B.x), make_float2(a.x, b.x));
+            const float2 y = then_map(make_float2(A.y, B.y), make_float2(a.y, b.y));
+            A = make_float2(x.x, y.x);
+            B = make_float2(x.y, y.y);
+        }
+    } else {
+        B = vfma(a, B, b);
+        A = vmul(A, a);
+    }
+}
+template <class V> __device__ __forceinline__ V apply_vec(V A, V B, V h) {
+    return vmap(A, B, h, [](float x, float y, float z) { return apply_map(x, y, z); });
+}
+
+// A carry warp: tiles c, c + kCarryWarps, ... of the block.  It is one warp's
+// dependent instructions that set the pace here, so before the wait it only
+// composes the warps' maps (leaving in their place the maps of what precedes
+// each warp) and publishes, and behind it stores one state per channel.
+// Forward (DIR +1): warps in order; the states entering the tile and its
+// second half are kept in p.states if given.  Backward (DIR -1): warps from
+// the last, and under the wait (map 1) the states of the forward recurrence
+// within the tile, from p.states.
 template <int E, int S, int TR, int DIR, class B>
 __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, int lane) {
+    using V = typename FVec<E>::type;
     Waiter wait{p.status, kTileWait};
     for (int n = c;; n += kCarryWarps) {
         wait(&blk.full[n % S], n / S);
@@ -425,68 +533,68 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
         if (info.tile >= p.n_tiles) return;
         const int64_t q = info.q, strip = info.strip;
         const bool fresh = DIR > 0 ? info.start[0] >= 0 : info.end[TR - 1] >= 0;
+        const bool cut = info.cut & (DIR > 0 ? 1 : 2), begins = info.cut & 1;
         const int e0 = n % kQ;
         const int64_t d0 = strip * 32 * E + lane * E;
-        float hf[E];
+        V hf = vset<V>(0.f);
         if constexpr (DIR < 0) {
             const int64_t chunk = p.n_chunks - 1 - q;
-            const bool begins = info.start[0] >= 0 || chunk == 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) hf[e] = begins || d0 + e >= p.D ? 0.f : p.states[chunk * p.D + d0 + e];
+            if (info.start[0] < 0 && chunk > 0) hf = state_row<E>(p.states, chunk * p.D, d0, p.D);
         }
         wait(&blk.maps[e0], n / kQ);
-        auto map_of = [&](int k, int w, int e) {
-            return make_float2(reinterpret_cast<const float *>(&blk.A[k][e0][w][lane])[e],
-                               reinterpret_cast<const float *>(&blk.B[k][e0][w][lane])[e]);
-        };
-        // the states entering each warp from those entering the tile
-        auto enter = [&](int k, bool up, float (&h)[E]) {
+        V A[kWarps], B_[kWarps];
 #pragma unroll
-            for (int j = 0; j < kWarps; ++j) {
-                const int w = up ? j : kWarps - 1 - j;
-                float *in = reinterpret_cast<float *>(&blk.enter[k][e0][w][lane]);
+        for (int w = 0; w < kWarps; ++w) {
+            A[w] = blk.A[0][e0][w][lane];
+            B_[w] = blk.B[0][e0][w][lane];
+        }
+        V tA = A[DIR > 0 ? 0 : kWarps - 1], tB = B_[DIR > 0 ? 0 : kWarps - 1];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float2 m = map_of(k, w, e);
-                    in[e] = h[e];
-                    h[e] = apply_map(m.x, m.y, h[e]);
-                }
-            }
-        };
+        for (int j = 1; j < kWarps; ++j) {
+            const int w = DIR > 0 ? j : kWarps - 1 - j;
+            const V a = A[w], b = B_[w];
+            blk.A[0][e0][w][lane] = tA;
+            blk.B[0][e0][w][lane] = tB;
+            compose(tA, tB, a, b, cut);
+        }
         float2 tot[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            tot[e] = map_of(0, DIR > 0 ? 0 : kWarps - 1, e);
-#pragma unroll
-            for (int j = 1; j < kWarps; ++j) tot[e] = then_map(tot[e], map_of(0, DIR > 0 ? j : kWarps - 1 - j, e));
-        }
         float hin[E];
-        carry_tile_state<E>(p, strip, q, lane, fresh, tot, hin, [&] {
-            if constexpr (DIR < 0) enter(1, true, hf);
-        });
-        float keep[2][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) keep[0][e] = hin[e];
-        enter(0, DIR > 0, hin);
-        if constexpr (DIR > 0) {
+        for (int e = 0; e < E; ++e)
+            tot[e] = make_float2(reinterpret_cast<const float *>(&tA)[e], reinterpret_cast<const float *>(&tB)[e]);
+        carry_tile_state<E>(p, strip, q, lane, fresh, cut, tot, hin, [&] {
+            if constexpr (DIR < 0) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                keep[1][e] = reinterpret_cast<const float *>(&blk.enter[0][e0][kWarps / 2][lane])[e];
-        }
-        __syncwarp();
-        if (lane == 0) arrive(&blk.in[e0]);
-        if constexpr (DIR > 0) {
-            if (p.states) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if ((2 * q + k) * kBwdTR >= p.rows) continue;
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (d0 + e < p.D) p.states[(2 * q + k) * p.D + d0 + e] = keep[k][e];
+                for (int w = 0; w < kWarps; ++w) {
+                    const V a = blk.A[1][e0][w][lane], b = blk.B[1][e0][w][lane];
+                    blk.A[1][e0][w][lane] = hf;
+                    hf = begins ? apply_vec(a, b, hf) : vfma(a, hf, b);
                 }
             }
+        });
+        V h;
+#pragma unroll
+        for (int e = 0; e < E; ++e) reinterpret_cast<float *>(&h)[e] = hin[e];
+        blk.enter[e0][lane] = h;
+        __syncwarp();
+        if constexpr (DIR > 0) {
+            // read before the data warps may go on to overwrite the maps
+            const V half = p.states ? apply_vec(blk.A[0][e0][kWarps / 2][lane], blk.B[0][e0][kWarps / 2][lane], h) : h;
+            if (lane == 0) arrive(&blk.in[e0]);
+            if (p.states) {
+                put_state_row<E>(p.states, 2 * q * p.D, d0, p.D, h);
+                if ((2 * q + 1) * kBwdTR < p.rows) put_state_row<E>(p.states, (2 * q + 1) * p.D, d0, p.D, half);
+            }
+        } else {
+            if (lane == 0) arrive(&blk.in[e0]);
         }
     }
+}
+
+// The state entering data warp w (in processing order the first: the tile's own)
+template <int FIRST, class B, class V>
+__device__ __forceinline__ V entering(const B &blk, int e0, int warp, int lane, V h) {
+    return warp == FIRST ? h : apply_vec(blk.A[0][e0][warp][lane], blk.B[0][e0][warp][lane], h);
 }
 
 // The thread's row r of an operand: from the slot, or from memory.
@@ -623,7 +731,7 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
             char *dst = static_cast<char *>(p.h) + (row * p.h_rs + d0) * int64_t(sizeof(IO));
             const int64_t pitch = p.h_rs * int64_t(sizeof(IO));
             const bool got = wait(&blk.in[n % kQ], n / kQ);
-            V h = got ? blk.enter[0][n % kQ][warp][lane] : vset<V>(nan_value());
+            V h = got ? entering<0>(blk, n % kQ, warp, lane, blk.enter[n % kQ][lane]) : vset<V>(nan_value());
             if (k.w) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -775,7 +883,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             const uint4 k = info.masks[warp];
             const bool dvalid = d0 < p.D;
             const bool got = wait(&blk.in[n % kQ], n / kQ);
-            V h = blk.enter[1][n % kQ][warp][lane];
+            V h = blk.A[1][n % kQ][warp][lane];
             V c[R];                                                   // df = c g
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -791,7 +899,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                     h = vfma(a, h, x);
                 }
             }
-            V flow = got ? blk.enter[0][n % kQ][warp][lane] : vset<V>(nan_value());
+            V flow = got ? entering<kWarps - 1>(blk, n % kQ, warp, lane, blk.enter[n % kQ][lane]) : vset<V>(nan_value());
             char *pf = static_cast<char *>(p.df) + ((row + R - 1) * p.df_rs + d0) * int64_t(sizeof(IO));
             char *pv = static_cast<char *>(p.dv) + ((row + R - 1) * p.dv_rs + d0) * int64_t(sizeof(IO));
             const int64_t pitch_f = p.df_rs * int64_t(sizeof(IO)), pitch_v = p.dv_rs * int64_t(sizeof(IO));
