@@ -607,9 +607,9 @@ SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
  *                state for every sequence); NULL: 0.
  *   h          : (rows, D) in dtype.  h_last: fp32 (n_seqs, D), the state behind
  *                each sequence (h0 where it is empty), or NULL.
- *   states     : fp32 (sgr_gated_chunks(rows), D): the state entering every
- *                chunk of 96 rows, what gated_scan_backward starts from (unused, and
- *                0, where the chunk begins with a sequence), or NULL.
+ *   states     : fp32 (sgr_gated_chunks(rows), D), or NULL: the states inside the
+ *                sequences that gated_scan_backward starts from, one per 96 rows
+ *                or so, in an order of its own.
  *   workspace  : sgr_gated_workspace_size(rows, D) bytes; need not be
  *                initialised and keeps nothing from call to call.  Not to be
  *                shared with another call that can run at the same time, nor

@@ -23,14 +23,16 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Workspace: header, then the words through which tiles hand their maps and
 // final states on.  Every byte is set to ~0 on the stream before the launch.
+// The rows fall into segments, each of whole chunks, so up to segs - 1 chunks
+// come on top of the rows' own.
 struct Layout {
     int64_t n_strips, n_chunks, n_tiles;
     size_t maps, carry, total;
 };
-Layout layout(int64_t rows, int64_t D, int tc, int tr) {
+Layout layout(int64_t rows, int64_t D, int tc, int tr, int segs) {
     Layout l;
     l.n_strips = (D + tc - 1) / tc;
-    l.n_chunks = (rows + tr - 1) / tr;
+    l.n_chunks = rows <= tr ? 1 : (rows + tr - 1) / tr + segs - 1;
     l.n_tiles = l.n_strips * l.n_chunks;
     l.maps = kHeader;
     l.carry = l.maps + size_t(l.n_tiles) * tc * 8;
@@ -38,11 +40,22 @@ Layout layout(int64_t rows, int64_t D, int tc, int tr) {
     return l;
 }
 
+// Segments to work on side by side: enough that a tile's predecessor is two
+// rounds of blocks older, and none shorter than eight tiles (each ends in a
+// partial one).  A function of the sizes alone: both directions share it, and
+// with it the places of the kept states.
+int segments(int64_t rows, int64_t D, int64_t n_seqs, int esz) {
+    constexpr int64_t kBlocks = 148;
+    const int64_t strips = (D * esz + 127) / 128;
+    return int(std::max<int64_t>(1, std::min<int64_t>({int64_t(kSegs), (2 * kBlocks + strips - 1) / strips,
+                                                       rows / (8 * kTR), n_seqs})));
+}
+
 bool sizes_ok(int64_t rows, int64_t D) {
     int64_t n = 0;
     // 16 bytes an element covers the workspace and every dense array
     return rows <= kMaxRows && D <= (int64_t(1) << 31) - 64 && host::mul_ok(rows, D, &n) && host::mul_ok(n, 16, &n) &&
-           ((rows + kBwdTR - 1) / kBwdTR) * ((D + 31) / 32) <= std::numeric_limits<int>::max();
+           ((rows + kBwdTR - 1) / kBwdTR + kSegs) * ((D + 31) / 32) <= std::numeric_limits<int>::max() / 2;
 }
 
 // Tensor map of (rows, D) for boxes of 128 bytes x tr rows; what lies past
@@ -70,12 +83,14 @@ cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int sms = host::sm_count(dev);
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int64_t most = p.ticket ? int64_t(sms) : p.n_tiles;
-    const unsigned grid = unsigned(std::max<int64_t>(1, std::min(p.n_tiles, most)));
+    const int tr = backward ? kBwdTR : kTR;
+    const int64_t chunks = (p.rows + tr - 1) / tr;
+    const int64_t tiles = p.n_strips * (chunks + p.n_segs - 1);
+    const unsigned grid = unsigned(std::max<int64_t>(1, p.ticket ? std::min<int64_t>(tiles, sms) : tiles));
     CUtensorMap m[3];
     std::memset(m, 0, sizeof(m));
     if (TMA) {
-        const int esz = sizeof(IO), tr = backward ? kBwdTR : kTR;
+        const int esz = sizeof(IO);
         if (!tile_map(&m[0], p.f, p.rows, p.D, p.f_rs, esz, tr) || !tile_map(&m[1], p.v, p.rows, p.D, p.v_rs, esz, tr) ||
             (backward && !tile_map(&m[2], p.dh, p.rows, p.D, p.dh_rs, esz, tr)))
             return cudaErrorInvalidValue;
@@ -130,7 +145,7 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
     if (p.f_rs < 0 || p.v_rs < 0 || p.h_rs < 0 || p.dh_rs < 0 || p.df_rs < 0 || p.dv_rs < 0) return SGR_ERR_INVALID_ARG;
     if (!sizes_ok(p.rows, p.D) || p.n_seqs > std::numeric_limits<int>::max()) return SGR_ERR_UNSUPPORTED;
     const int tr = backward ? kBwdTR : kTR;
-    const int64_t n_chunks = (p.rows + tr - 1) / tr, n_states = (p.rows + kBwdTR - 1) / kBwdTR;
+    const int64_t n_chunks = (p.rows + tr - 1) / tr, n_states = sgr_gated_chunks(p.rows);
     if (p.rows > 0) {
         if (!p.f || !p.v) return SGR_ERR_INVALID_ARG;
         if (backward ? (!p.dh || !p.df || !p.dv || (n_chunks > 1 && !p.states)) : !p.h) return SGR_ERR_INVALID_ARG;
@@ -154,10 +169,9 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
             four = four && host::aligned(q, 4);
         E = (odd & 1) == 0 && four ? 2 : 1;
     }
-    const Layout l = layout(p.rows, p.D, 32 * E, tr);
+    p.n_segs = segments(p.rows, p.D, p.n_seqs, esz);
+    const Layout l = layout(p.rows, p.D, 32 * E, tr, p.n_segs);
     p.n_strips = l.n_strips;
-    p.n_chunks = l.n_chunks;
-    p.n_tiles = l.n_tiles;
     p.seq_rows = p.cu ? 1u : uint32_t(p.rows / std::max<int64_t>(1, p.n_seqs));
     p.spin_limit = kSpinLimit;
     Span out[4], in[8];
@@ -165,18 +179,18 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
         out[0] = {p.df, b_df};
         out[1] = {p.dv, b_dv};
         out[2] = {p.dh0, b_seq};
-        out[3] = {ws, p.n_chunks > 1 ? int64_t(l.total) : 0};
+        out[3] = {ws, n_chunks > 1 ? int64_t(l.total) : 0};
     } else {
         out[0] = {p.h, b_h};
         out[1] = {p.h_last, b_seq};
         out[2] = {p.states, b_st};
-        out[3] = {ws, p.n_chunks > 1 ? int64_t(l.total) : 0};
+        out[3] = {ws, n_chunks > 1 ? int64_t(l.total) : 0};
     }
     const Span ins[8] = {{p.f, b_f}, {p.v, b_v}, {p.dh, b_dh}, {p.h0, b_h0}, {p.dh_last, b_seq}, {p.cu, b_cu},
                          {backward ? p.states : nullptr, b_st}, {nullptr, 0}};
     std::copy(ins, ins + 8, in);
     if (host::any_overlap(out, in)) return SGR_ERR_INVALID_ARG;
-    if (p.n_chunks > 1) {
+    if (n_chunks > 1) {
         if (!ws || ws_bytes < l.total || !host::aligned(ws, 16)) return SGR_ERR_WORKSPACE;
         char *w = static_cast<char *>(ws);
         p.status = reinterpret_cast<uint32_t *>(w);
@@ -201,11 +215,11 @@ void launch_step(const StepParams &p, int gate, unsigned grid, cudaStream_t s) {
 
 extern "C" {
 
-int64_t sgr_gated_chunks(int64_t rows) { return rows <= 0 ? 0 : (rows + kBwdTR - 1) / kBwdTR; }
+int64_t sgr_gated_chunks(int64_t rows) { return rows <= 0 ? 0 : rows <= kBwdTR ? 1 : (rows + kBwdTR - 1) / kBwdTR + kSegs - 1; }
 
 size_t sgr_gated_workspace_size(int64_t rows, int64_t D) {
     if (rows <= kBwdTR || D <= 0 || !sizes_ok(rows, D)) return 0;
-    return std::max(layout(rows, D, 32, kBwdTR).total, layout(rows, D, 64, kBwdTR).total);
+    return std::max(layout(rows, D, 32, kBwdTR, kSegs).total, layout(rows, D, 64, kBwdTR, kSegs).total);
 }
 
 sgr_status_t gated_scan(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride, const float *h0,

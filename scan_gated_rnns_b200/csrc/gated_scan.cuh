@@ -19,7 +19,12 @@
 // the nearest earlier tile whose final state is published, applies the maps
 // between, oldest first, and publishes its own final state.  The arithmetic
 // is the sequential S_q = A_q S_{q-1} + B_q wherever that state came from, so
-// results do not depend on timing.  A map is one 64-bit word, a state one
+// results do not depend on timing.  To have the state there when it is asked
+// for, the rows are cut at sequence starts into segments of about equal length
+// and the segments are worked on side by side, so that a tile's predecessor is
+// a round of blocks older (one segment: 64 strips of bf16 32768 x 4096 in 23
+// sequences waited 2.6 us a tile, half of that for the predecessor's own
+// fold).  A map is one 64-bit word, a state one
 // 32-bit word per channel, all of them ~0 before the launch and valid once
 // they are not (arithmetic never gives that NaN), so a look-back is one round
 // trip to L2, without flags or fences.  Blocks take tiles by ticket in the
@@ -41,6 +46,8 @@
 
 #include "gated_math.cuh"
 
+#include <limits.h>
+
 namespace sgr {
 namespace gated {
 
@@ -54,6 +61,7 @@ constexpr int kSlots = 4, kBwdSlots = 5;   // tiles in shared memory
 constexpr int kQ = 2;                      // tiles between fold and the end of their replay
 constexpr uint32_t kTileWait = 1u << 16;   // polls of a wait inside the block (each suspends for tens of us)
 static_assert(kTR == 2 * kBwdTR, "a forward tile holds two saved states");
+constexpr int kSegs = 32;                  // most segments: one per lane of the feeding warp
 constexpr uint32_t kNone = 0xffffffffu;    // a word not yet published
 
 struct GatedParams {
@@ -66,16 +74,17 @@ struct GatedParams {
     float *h_last;                         // (n_seqs, D) or null
     const float *dh_last;                  // (n_seqs, D) or null
     float *dh0;                            // (n_seqs, D) or null
-    float *states;                         // (ceil(rows / kBwdTR), D): state entering each, or null (forward)
+    float *states;                         // state entering every kBwdTR rows of each segment, or null (forward)
     const void *cu;                        // n_seqs + 1 row bounds, or null: sequences of seq_rows rows
     int cu_bytes;                          // 4 or 8
     uint32_t seq_rows;
     int64_t rows, D, n_seqs;
-    int64_t n_strips, n_chunks, n_tiles;
+    int64_t n_strips;
+    int n_segs;                            // at most kSegs
     int zero_padding;                      // outputs of rows in no sequence: 0 written, else left
-    uint64_t *maps;                        // [n_tiles][TC] words (A, B), ~0 at launch
-    uint32_t *carry;                       // [n_tiles][TC] words: state leaving each tile, ~0 at launch
-    uint32_t *ticket;                      // ~0 at launch, or null: tile = blockIdx.x
+    uint64_t *maps;                        // [tiles][TC] words (A, B), ~0 at launch
+    uint32_t *carry;                       // [tiles][TC] words: state leaving each tile, ~0 at launch
+    uint32_t *ticket;                      // ~0 at launch, or null: one chunk, tile = blockIdx.x
     uint32_t *status;                      // ~0 at launch; SGR_ERR_TIMEOUT once a wait ran out; may be null
     uint32_t spin_limit;
 };
@@ -104,25 +113,39 @@ __device__ __forceinline__ float2 then_map(float2 first, float2 then) {
 
 // What the feeding warp tells the others of a tile.
 template <int TR> struct TileInfo {
-    int64_t tile, row0;                    // tile n_tiles: no more
-    int strip, q;                          // its strip, and its place along it in processing order
+    int64_t row0, row_end;                 // its rows (fewer than TR at the end of a segment)
+    int64_t state_row;                     // place of its first row's state in `states`
+    int there;                             // 0: no more tiles
+    int strip, place, word;                // strip; chunk in processing order within the segment, and of all
+    int last;                              // nothing of its segment follows
     int cut;                               // a sequence starts (1) or ends (2) in the tile
     uint4 masks[kWarps];                   // of each data warp's rows: starts, ends, in a sequence; .w: all plain
     int start[TR], end[TR];                // sequence that starts (ends) at the row, or -1
 };
 
-// Fill the table of the tile of rows [row0, row0 + TR) (whole warp).  Bounds
+// Fill the table of the tile of rows [row0, row_end) (whole warp).  Bounds
 // that are not ascending give wrong sequences but never a row or a sequence
 // outside the buffers.
 template <int TR>
-__device__ __forceinline__ void fill_info(const GatedParams &p, const Bounds &cu, int64_t row0, TileInfo<TR> &t, int lane) {
+__device__ __forceinline__ void fill_info(const GatedParams &p, const Bounds &cu, int64_t row0, int64_t row_end,
+                                          TileInfo<TR> &t, int lane) {
     constexpr int R = TR / kWarps;
-    const int64_t row_end = row0 + TR < p.rows ? row0 + TR : p.rows;
     int64_t lo_row = 0, hi_row = p.rows;   // rows that lie in sequences
+    constexpr uint32_t all = (1u << R) - 1u;
+    // most tiles lie inside one sequence: nothing starts or ends in them, and no row is looked at
+    auto plain = [&] {
+        if (lane < kWarps) t.masks[lane] = make_uint4(0u, 0u, all, 1u);
+        if (lane == 0) {
+            t.cut = 0;
+            t.start[0] = t.end[TR - 1] = -1;
+        }
+    };
     if (p.cu == nullptr) {
+        const uint32_t s0 = uint32_t(row0) / p.seq_rows, k0 = uint32_t(row0) - s0 * p.seq_rows;
+        if (k0 > 0 && k0 + TR < p.seq_rows) return plain();
         uint32_t s = uint32_t(row0 + lane) / p.seq_rows, k = uint32_t(row0 + lane) - s * p.seq_rows;
         for (int r = lane; r < TR; r += 32) {
-            const bool in = row0 + r < p.rows;
+            const bool in = row0 + r < row_end;
             t.start[r] = in && k == 0 ? int(s) : -1;
             t.end[r] = in && k + 1 == p.seq_rows ? int(s) : -1;
             k += 32;
@@ -133,10 +156,6 @@ __device__ __forceinline__ void fill_info(const GatedParams &p, const Bounds &cu
             }
         }
     } else {
-        for (int r = lane; r < TR; r += 32) t.start[r] = t.end[r] = -1;
-        lo_row = cu(0);
-        const int64_t last = cu(p.n_seqs);
-        hi_row = last < p.rows ? last : p.rows;
         // bounds at or below row0, by a 33-way search: the last of them begins the
         // sequence that holds row0
         int lo = 0, hi = int(p.n_seqs) + 1;
@@ -150,6 +169,11 @@ __device__ __forceinline__ void fill_info(const GatedParams &p, const Bounds &cu
             lo = int(next < hi ? next : hi);
             hi = int(top < hi ? top : hi);
         }
+        if (lo > 0 && lo <= p.n_seqs && cu(lo - 1) < row0 && cu(lo) > row0 + TR && row0 + TR <= row_end) return plain();
+        lo_row = cu(0);
+        const int64_t last = cu(p.n_seqs);
+        hi_row = last < p.rows ? last : p.rows;
+        for (int r = lane; r < TR; r += 32) t.start[r] = t.end[r] = -1;
         __syncwarp();
         for (int64_t s = (lo > 0 ? lo - 1 : 0) + lane;; s += 32) {
             bool more = false;
@@ -171,10 +195,9 @@ __device__ __forceinline__ void fill_info(const GatedParams &p, const Bounds &cu
         const int r = r0 + lane;
         const uint32_t starts = __ballot_sync(0xffffffffu, r < TR && t.start[r < TR ? r : 0] >= 0);
         const uint32_t ends = __ballot_sync(0xffffffffu, r < TR && t.end[r < TR ? r : 0] >= 0);
-        const uint32_t live = __ballot_sync(0xffffffffu, r < TR && row0 + r >= lo_row && row0 + r < hi_row);
+        const uint32_t live = __ballot_sync(0xffffffffu, r < TR && row0 + r >= lo_row && row0 + r < hi_row && row0 + r < row_end);
         cut |= (starts ? 1 : 0) | (ends ? 2 : 0);
         if (lane < 32 / R && r0 / R + lane < kWarps) {
-            constexpr uint32_t all = (1u << R) - 1u;
             const uint32_t a = starts >> (lane * R) & all, b = ends >> (lane * R) & all, c = live >> (lane * R) & all;
             t.masks[r0 / R + lane] = make_uint4(a, b, c, a == 0u && b == 0u && c == all);
         }
@@ -225,8 +248,8 @@ template <int E> __device__ __forceinline__ void apply_words(const uint64_t (&m)
         h[e] = apply_map(__uint_as_float(uint32_t(m[e])), __uint_as_float(uint32_t(m[e] >> 32)), h[e]);
 }
 
-// The carry of one tile (carry warp): q its place in processing order along
-// its strip, tot the tile's maps of this lane's E channels.  Publishes,
+// The carry of one tile (carry warp): q its place in processing order within
+// its segment, word that of its words, tot the tile's maps of this lane's E channels.  Publishes,
 // waits, and returns the entering states.  Tiles whose first row (in
 // processing order) is a start enter with 0, which they never use.  One round
 // trip reads the words of the kNear tiles before for every channel, and those
@@ -236,12 +259,12 @@ template <int E> __device__ __forceinline__ void apply_words(const uint64_t (&m)
 // first.
 constexpr int kNear = 4;
 template <int E, class Meanwhile>
-__device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int64_t q, int lane, bool fresh,
-                                                 bool cut, const float2 (&tot)[E], float (&hin)[E], Meanwhile meanwhile) {
+__device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int q, int word, bool last, int lane,
+                                                 bool fresh, bool cut, const float2 (&tot)[E], float (&hin)[E],
+                                                 Meanwhile meanwhile) {
     constexpr int TC = 32 * E;
     const int64_t step = p.n_strips * TC;                          // from a tile's words to the next chunk's
-    const int64_t at = q * step + strip * TC + lane * E;
-    const bool last = q + 1 == p.n_chunks;
+    const int64_t at = word * step + strip * TC + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) hin[e] = 0.f;
     auto publish_state = [&] {
@@ -249,7 +272,7 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
 #pragma unroll
         for (int e = 0; e < E; ++e) st_relaxed_u32(p.carry + at + e, __float_as_uint(apply_map(tot[e].x, tot[e].y, hin[e])));
     };
-    if (fresh || q == 0) {
+    if (fresh) {
         publish_state();
         meanwhile();
         return;
@@ -274,12 +297,12 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
                 m[i][0] = ~uint64_t(0);
             }
         }
-        const int64_t far = q - 1 - kNear - lane;                  // the tile that this lane probes
+        const int far = 1 + kNear + lane;                          // this lane probes the tile that far before
         uint32_t ps = kNone;
         uint64_t pm = ~uint64_t(0);
-        if (far >= 0) {
-            ps = ld_relaxed_u32(p.carry + far * step + strip * TC);
-            pm = ld_relaxed_u64(p.maps + far * step + strip * TC);
+        if (q - far >= 0) {
+            ps = ld_relaxed_u32(p.carry + (word - far) * step + strip * TC);
+            pm = ld_relaxed_u64(p.maps + (word - far) * step + strip * TC);
         }
         if (polls == 0) meanwhile();
         int k = -1;                                                // nearest published state, maps there before it
@@ -436,10 +459,83 @@ struct SmemShape {
     static_assert(op_bytes % 128 == 0 && TR <= 256, "copy boxes");
 };
 
+// The segments, one per lane of the feeding warp: rows [start, start + len),
+// n chunks of TR rows.  Segment g begins at the sequence bound nearest to
+// rows g / n_segs, segment 0 at row 0.  A tile is found from its ticket in
+// order of the place within the segment, then the segment, then the strip.
+template <int TR> struct Segments {
+    int64_t start, len;
+    int n, word0, state0;                  // chunks; chunks and kept states of the segments before
+    int total;                             // chunks of all
+    int c, below;                          // place reached, and chunks at lower places
+
+    __device__ __forceinline__ void init(const GatedParams &p, const Bounds &cu, int lane) {
+        int64_t at = p.rows;
+        if (lane == 0) {
+            at = 0;
+        } else if (lane < p.n_segs) {
+            const int64_t ideal = p.rows / p.n_segs * lane;
+            if (p.cu == nullptr) {
+                at = (ideal + p.seq_rows / 2) / p.seq_rows * p.seq_rows;
+            } else {
+                int64_t lo = 0, hi = p.n_seqs + 1;                 // bounds at or below the ideal one
+                while (lo < hi) {
+                    const int64_t mid = (lo + hi) / 2;
+                    if (cu(mid) <= ideal) lo = mid + 1;
+                    else hi = mid;
+                }
+                const int64_t up = lo <= p.n_seqs ? cu(lo) : cu(p.n_seqs);
+                const int64_t down = lo > 0 ? cu(lo - 1) : up;
+                at = ideal - down <= up - ideal ? down : up;
+            }
+            if (at < 0) at = 0;
+            if (at > p.rows) at = p.rows;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {                         // ascending whatever the bounds are
+            const int64_t x = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o && x > at) at = x;
+        }
+        start = at;
+        const int64_t next = __shfl_down_sync(0xffffffffu, at, 1);
+        len = lane >= p.n_segs ? 0 : (lane == p.n_segs - 1 ? p.rows : next) - start;
+        n = int((len + TR - 1) / TR);
+        const int k = int((len + kBwdTR - 1) / kBwdTR);
+        int a = n, b = k;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+            if (lane >= o) {
+                a += x;
+                b += y;
+            }
+        }
+        word0 = a - n;
+        state0 = b - k;
+        total = __shfl_sync(0xffffffffu, a, 31);
+        c = below = 0;
+    }
+    // the segment of chunk `k` in processing order (k ascends from call to call, below total); c is its place
+    __device__ __forceinline__ int find(int k, int lane) {
+        uint32_t live = __ballot_sync(0xffffffffu, n > c);
+        while (k >= below + __popc(live)) {
+            const int cnt = __popc(live);
+            const int shortest = __reduce_min_sync(0xffffffffu, n > c ? n : INT_MAX);
+            const int want = (k - below) / cnt, most = shortest - c;
+            const int steps = want < most ? want : most;
+            c += steps;
+            below += steps * cnt;
+            live = __ballot_sync(0xffffffffu, n > c);
+        }
+        const int rank = __popc(live & ((1u << lane) - 1u));
+        return __ffs(__ballot_sync(0xffffffffu, n > c && rank == k - below)) - 1;
+    }
+};
+
 // The feeding warp: draws tickets, starts the copies of a tile when its slot
-// is free, writes its table and hands both over.  `reverse` counts chunks
-// from the last.  Ends with one entry for each carry warp whose tile is
-// n_tiles, so that each of them comes upon one.
+// is free, writes its table and hands both over.  `reverse`: places count
+// from the segment's end.  Ends with one entry for each carry warp that says
+// so, so that each of them comes upon one.
 template <int S, int OPS, int TR, uint32_t OP_BYTES, int TC, bool TMA, class B>
 __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slots, int lane, bool reverse,
                                      const CUtensorMap *m0, const CUtensorMap *m1, const CUtensorMap *m2) {
@@ -456,15 +552,24 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
         for (int i = lane; i <= int(p.n_seqs); i += 32) blk.bounds[i] = cu_at(p, i);
     const Bounds bounds{p, held ? blk.bounds : nullptr};
     __syncwarp();
+    Segments<TR> seg;
+    seg.init(p, bounds, lane);
     int ends = 0;
     for (int n = 0; ends < kCarryWarps; ++n) {
         const uint32_t tile = __shfl_sync(0xffffffffu, ticket, 0);
-        const bool more = ends == 0 && tile < uint32_t(p.n_tiles);
+        const uint32_t k = tile / uint32_t(p.n_strips), strip = tile - k * uint32_t(p.n_strips);
+        const bool more = ends == 0 && k < uint32_t(seg.total);
+        int g = 0;
+        if (more) g = seg.find(int(k), lane);
+        const int count = __shfl_sync(0xffffffffu, seg.n, g);
+        const int c = reverse ? count - 1 - seg.c : seg.c;                      // chunk of the segment
+        const int64_t from = __shfl_sync(0xffffffffu, seg.start, g), len = __shfl_sync(0xffffffffu, seg.len, g);
+        const int word = __shfl_sync(0xffffffffu, seg.word0, g) + seg.c;
+        const int state = __shfl_sync(0xffffffffu, seg.state0, g) + c * (TR / kBwdTR);
+        const int64_t row0 = from + int64_t(c) * TR, end = from + len, row_end = row0 + TR < end ? row0 + TR : end;
         if (n >= S) wait(&blk.empty[n % S], n / S - 1);
         TileInfo<TR> &info = blk.info[n % S];
         if (more) {
-            const uint32_t q = tile / uint32_t(p.n_strips), strip = tile - q * uint32_t(p.n_strips);
-            const int64_t row0 = int64_t(reverse ? uint32_t(p.n_chunks) - 1 - q : q) * TR;
             if (lane == 0) {
                 if constexpr (TMA) {
                     const uint32_t bar = smem_addr(&blk.full[n % S]);
@@ -477,17 +582,21 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
                     tma_load_2d(dst + OP_BYTES, m1, int(strip) * TC, int(row0), bar);
                     if constexpr (OPS == 3) tma_load_2d(dst + 2 * OP_BYTES, m2, int(strip) * TC, int(row0), bar);
                 }
-                ticket = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : uint32_t(p.n_tiles);
+                ticket = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : uint32_t(p.n_strips);
                 info.row0 = row0;
+                info.row_end = row_end;
+                info.state_row = state;
                 info.strip = int(strip);
-                info.q = int(q);
+                info.place = seg.c;
+                info.word = word;
+                info.last = seg.c + 1 == count;
             }
             __syncwarp();
-            fill_info<TR>(p, bounds, row0, info, lane);
+            fill_info<TR>(p, bounds, row0, row_end, info, lane);
         } else {
             ++ends;
         }
-        if (lane == 0) info.tile = more ? int64_t(tile) : p.n_tiles;
+        if (lane == 0) info.there = more;
         __syncwarp();
         if (lane == 0) arrive(&blk.full[n % S]);
     }
@@ -530,16 +639,17 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
     for (int n = c;; n += kCarryWarps) {
         wait(&blk.full[n % S], n / S);
         const TileInfo<TR> &info = blk.info[n % S];
-        if (info.tile >= p.n_tiles) return;
-        const int64_t q = info.q, strip = info.strip;
-        const bool fresh = DIR > 0 ? info.start[0] >= 0 : info.end[TR - 1] >= 0;
+        if (!info.there) return;
+        const int64_t strip = info.strip, state = info.state_row;
+        const int q = info.place, word = info.word;
+        const bool fresh = q == 0 || (DIR > 0 ? info.start[0] : info.end[TR - 1]) >= 0, last = info.last;
+        const bool halves = info.row0 + kBwdTR < info.row_end;
         const bool cut = info.cut & (DIR > 0 ? 1 : 2), begins = info.cut & 1;
         const int e0 = n % kQ;
         const int64_t d0 = strip * 32 * E + lane * E;
         V hf = vset<V>(0.f);
         if constexpr (DIR < 0) {
-            const int64_t chunk = p.n_chunks - 1 - q;
-            if (info.start[0] < 0 && chunk > 0) hf = state_row<E>(p.states, chunk * p.D, d0, p.D);
+            if (info.start[0] < 0 && !last) hf = state_row<E>(p.states, state * p.D, d0, p.D);
         }
         wait(&blk.maps[e0], n / kQ);
         V A[kWarps], B_[kWarps];
@@ -562,7 +672,7 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
 #pragma unroll
         for (int e = 0; e < E; ++e)
             tot[e] = make_float2(reinterpret_cast<const float *>(&tA)[e], reinterpret_cast<const float *>(&tB)[e]);
-        carry_tile_state<E>(p, strip, q, lane, fresh, cut, tot, hin, [&] {
+        carry_tile_state<E>(p, strip, q, word, last, lane, fresh, cut, tot, hin, [&] {
             if constexpr (DIR < 0) {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
@@ -582,8 +692,8 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
             const V half = p.states ? apply_vec(blk.A[0][e0][kWarps / 2][lane], blk.B[0][e0][kWarps / 2][lane], h) : h;
             if (lane == 0) arrive(&blk.in[e0]);
             if (p.states) {
-                put_state_row<E>(p.states, 2 * q * p.D, d0, p.D, h);
-                if ((2 * q + 1) * kBwdTR < p.rows) put_state_row<E>(p.states, (2 * q + 1) * p.D, d0, p.D, half);
+                put_state_row<E>(p.states, state * p.D, d0, p.D, h);
+                if (halves) put_state_row<E>(p.states, (state + 1) * p.D, d0, p.D, half);
             }
         } else {
             if (lane == 0) arrive(&blk.in[e0]);
@@ -686,7 +796,7 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
         auto fold = [&](int n, V (&g)[R]) {
             const bool got = wait(&blk.full[n % S], n / S);
             const TileInfo<kTR> &info = blk.info[n % S];
-            if (info.tile >= p.n_tiles) return false;
+            if (!info.there) return false;
             const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
             const auto f = reader<IO, E, TMA, R, Shape, 0>(p, smem, n % S, warp, lane, row, d0, p.f, p.f_rs);
             const auto v = reader<IO, E, TMA, R, Shape, 1>(p, smem, n % S, warp, lane, row, d0, p.v, p.v_rs);
@@ -748,7 +858,7 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
                     fwd_step<GATE, IO>(g[r], v(r), a, b);
                     if (k.x >> r & 1u) h = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
                     h = vfma(a, h, b);
-                    if (dvalid && row + r < p.rows) {
+                    if (dvalid && row + r < info.row_end) {
                         if (k.z >> r & 1u) __stcs(reinterpret_cast<W *>(dst), C::out(h));
                         else if (p.zero_padding) __stcs(reinterpret_cast<W *>(dst), W(0));
                     }
@@ -836,7 +946,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
         auto fold = [&](int n, V (&s)[R]) {
             const bool got = wait(&blk.full[n % S], n / S);
             const TileInfo<kBwdTR> &info = blk.info[n % S];
-            if (info.tile >= p.n_tiles) return false;
+            if (!info.there) return false;
             const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
             const auto f = reader<IO, E, TMA, R, Shape, 0>(p, smem, n % S, warp, lane, row, d0, p.f, p.f_rs);
             const auto v = reader<IO, E, TMA, R, Shape, 1>(p, smem, n % S, warp, lane, row, d0, p.v, p.v_rs);
@@ -924,7 +1034,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                     const V g = vadd(flow, dh(r));
                     V a, z;
                     bwd_split<GATE>(s[r], a, z);
-                    if (dvalid && row + r < p.rows) {
+                    if (dvalid && row + r < info.row_end) {
                         const bool live = k.z >> r & 1u;
                         __stcs(reinterpret_cast<W *>(pf), live ? C::out(vmul(c[r], g)) : W(0));
                         __stcs(reinterpret_cast<W *>(pv), live ? C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g) : W(0));

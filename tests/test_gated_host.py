@@ -40,12 +40,12 @@ def test_reference_gradients_against_differences(gate):
 
 
 # ------------------------------------------------- bounds search, replayed
-def fill_info(cu, rows, row0):
+def fill_info(cu, rows, row0, row_end=None):
     """The table of a tile, lane by lane as the kernel fills it; every index is
     checked against its array."""
     n_seqs = len(cu) - 1
     start, end = [-1] * TR, [-1] * TR
-    row_end = min(row0 + TR, rows)
+    row_end = min(row0 + TR, rows) if row_end is None else row_end
 
     def at(i):
         assert 0 <= i <= n_seqs
@@ -106,9 +106,71 @@ def test_bounds_in_no_order_stay_inside_the_arrays():
                 assert all(-1 <= s < seqs for s in start + end)
 
 
+def segments(cu, rows, n_segs, tr):
+    """(start, length, chunks, place of the first) of each segment, as the
+    feeding warp finds them from any bounds."""
+    n_seqs = len(cu) - 1
+    clamp = [max(-1, min(rows + 1, b)) for b in cu]
+    at = [0]
+    for g in range(1, n_segs):
+        ideal = rows // n_segs * g
+        lo, hi = 0, n_seqs + 1
+        while lo < hi:
+            mid = (lo + hi) // 2
+            if clamp[mid] <= ideal:
+                lo = mid + 1
+            else:
+                hi = mid
+        up = clamp[lo] if lo <= n_seqs else clamp[n_seqs]
+        down = clamp[lo - 1] if lo > 0 else up
+        x = down if ideal - down <= up - ideal else up
+        at.append(max(at[-1], min(rows, max(0, x))))
+    lens = [b - a for a, b in zip(at, at[1:] + [rows])]
+    chunks = [-(-n // tr) for n in lens]
+    return at, lens, chunks, [sum(chunks[:g]) for g in range(n_segs)]
+
+
+def tiles_in_order(chunks):
+    """(segment, place) of each chunk in processing order, by the kernel's stepping."""
+    c = below = 0
+    for k in range(sum(chunks)):
+        live = [n > c for n in chunks]
+        while k >= below + sum(live):
+            steps = min((k - below) // sum(live), min(n for n in chunks if n > c) - c)
+            c, below = c + steps, below + steps * sum(live)
+            live = [n > c for n in chunks]
+        yield [g for g, on in enumerate(live) if on][k - below], c
+
+
+@pytest.mark.parametrize("n_segs", [1, 2, 5, 17, 32])
+def test_segments_cover_the_rows_once_and_wait_for_earlier_tiles_only(n_segs):
+    rng = np.random.default_rng(n_segs)
+    for rows in (1, 500, 9001):
+        for tr in (TR, 2 * TR):
+            for trial in range(6):
+                cu = np.sort(rng.integers(0, rows + 1, rng.integers(1, 60))).tolist()
+                if trial == 4:
+                    cu = [0, rows]
+                if trial == 5:                          # in no order, out of range
+                    cu = rng.integers(-rows, 3 * rows, 20).tolist()
+                at, lens, chunks, first = segments(cu, rows, n_segs, tr)
+                assert at[0] == 0 and sum(lens) == rows and min(lens) >= 0
+                assert sum(chunks) <= -(-rows // tr) + n_segs - 1
+                assert sum(-(-n // TR) for n in lens) <= _abi.lib().sgr_gated_chunks(rows) or n_segs > 1 and rows <= TR
+                if trial < 5:                           # a segment never begins inside a sequence
+                    inside = {r for b, e in zip(cu, cu[1:]) for r in range(b + 1, e)}
+                    assert not inside & {a for a, n in zip(at, lens) if n}
+                order = list(tiles_in_order(chunks))
+                assert sorted(order) == sorted((g, c) for g, n in enumerate(chunks) for c in range(n))
+                seen = set()
+                for g, c in order:                      # the place before it in its segment came first
+                    assert c == 0 or (g, c - 1) in seen
+                    seen.add((g, c))
+
+
 def test_chunks_and_workspace_sizes():
     lib = _abi.lib()
-    assert [lib.sgr_gated_chunks(n) for n in (-1, 0, 1, TR, TR + 1, 10 * TR)] == [0, 0, 1, 1, 2, 10]
+    assert [lib.sgr_gated_chunks(n) for n in (-1, 0, 1, TR, TR + 1, 10 * TR)] == [0, 0, 1, 1, 33, 41]
     assert lib.sgr_gated_workspace_size(TR, 4096) == 0
     need = lib.sgr_gated_workspace_size(1000, 100)
     assert need >= 256 + 11 * 128 * 12

@@ -426,3 +426,34 @@ def test_step_captured():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(state, want)
+
+
+# ------------------------------------------------------------- segments
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bounds", [
+    [0, 4000, 4001, 9000, 9000, 15000, 16001],              # many segments, at uneven bounds
+    [0, 16001],                                             # one sequence: one segment's worth
+    [5, 100, 15900],                                        # a short first sequence, padding at both ends
+    list(range(0, 16002, 127)) + [16001],                   # sequences shorter than a tile
+])
+def test_rows_cut_into_segments(bounds, dtype):
+    rng = np.random.default_rng(len(bounds))
+    rows, D, n = 16001, 24, len(bounds) - 1
+    f, v, f64, v64 = make(rng, "sigmoid", rows, D, dtype)
+    h0 = rng.normal(size=(n, D)).astype(np.float32)
+    h0_d, cu = torch.from_numpy(h0).to(DEV), torch.tensor(bounds, device=DEV)
+    h, last, states = sgr.gated_scan(f, v, h0_d, cu, save_states=True)
+    want, wl, bh, bl = scan64(f64, v64, h0.astype(np.float64), bounds, "sigmoid", dtype)
+    check(h, want, bh, dtype, "h")
+    check(last, wl, bl, F32, "h_last")
+    dh = torch.from_numpy(rng.normal(size=(rows, D))).to(dtype)
+    df, dv, d0 = sgr.gated_scan_backward(f, v, h0_d, states, dh.to(DEV), None, cu)
+    wf, wv, w0, bf, bv, b0 = grad64(f64, v64, h0.astype(np.float64), bounds, "sigmoid", dh.double().numpy(), None, dtype)
+    check(df, wf, bf, dtype, "df")
+    check(dv, wv, bv, dtype, "dv")
+    check(d0, w0, b0, F32, "dh0")
+    # an upstream gradient on unaligned rows takes another path than the forward did: the same places of the states
+    odd = torch.zeros(rows, D + 1, dtype=dtype, device=DEV)[:, 1:]
+    odd.copy_(dh)
+    for a, b in zip(sgr.gated_scan_backward(f, v, h0_d, states, odd, None, cu), (df, dv, d0)):
+        assert torch.equal(a, b) or torch.allclose(a.float(), b.float(), rtol=0.02, atol=1e-4)
