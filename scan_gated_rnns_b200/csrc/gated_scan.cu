@@ -99,15 +99,13 @@ cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
         constexpr uint32_t bytes = BackwardShape<IO, E, TMA>::smem_bytes;
         auto kernel = gated_scan_backward_kernel<IO, E, GATE, TMA>;
         static_assert(bytes <= 227 * 1024, "one block per SM");
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
-            return e;
+        if ((e = host::allow_smem<gated_scan_backward_kernel<IO, E, GATE, TMA>>(int(bytes))) != cudaSuccess) return e;
         kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1], m[2]);
     } else {
         constexpr uint32_t bytes = ForwardShape<IO, E, TMA>::smem_bytes;
         auto kernel = gated_scan_kernel<IO, E, GATE, TMA>;
         static_assert(bytes <= 227 * 1024, "one block per SM");
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))) != cudaSuccess)
-            return e;
+        if ((e = host::allow_smem<gated_scan_kernel<IO, E, GATE, TMA>>(int(bytes))) != cudaSuccess) return e;
         kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1]);
     }
     return cudaGetLastError();

@@ -82,6 +82,20 @@ inline EncodeTiledFn encode_tiled() {
     return f;
 }
 
+// Dynamic shared memory of a kernel, set once per kernel and device.
+template <auto KERNEL>
+inline cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (done.load() & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
 inline int float_size(sgr_dtype_t t) { return t == SGR_F32 ? 4 : (t == SGR_BF16 || t == SGR_F16 ? 2 : 0); }
 
 }  // namespace host

@@ -23,11 +23,30 @@ inline int64_t pad16(int64_t n) { return (n + 15) / 16 * 16; }
 size_t quant_bytes(int64_t M, int64_t K) { return size_t(M) * size_t(pad16(K)); }
 size_t scale_at(int64_t M, int64_t K) { return (quant_bytes(M, K) + 255) / 256 * 256; }
 
+template <typename IO, int TPR, int NV>
+void launch_quantize(const QuantParams &p, cudaStream_t s) {
+    const int64_t blocks = (p.rows + 256 / TPR - 1) / (256 / TPR);
+    int8_quantize_kernel<IO, TPR, NV><<<unsigned(std::min<int64_t>(blocks, 148 * 32)), 256, 0, s>>>(p);
+}
+// A warp per row up to 4 vectors a lane, a block up to 4 a thread (bf16: rows of 1024 and 8192 values).
+template <typename IO>
+void quantize_rows(const QuantParams &p, cudaStream_t s) {
+    constexpr int VEC = 16 / sizeof(IO);
+    const bool vec = host::aligned(p.x, 16) && host::aligned(p.q, 16) &&
+                     (p.rows <= 1 || (p.x_rs * int64_t(sizeof(IO)) % 16 == 0 && p.q_rs % 16 == 0));
+    const int64_t n = (p.K + VEC - 1) / VEC;
+    if (!vec || n > 4 * 256) launch_quantize<IO, 256, 0>(p, s);
+    else if (n <= 32) launch_quantize<IO, 32, 1>(p, s);
+    else if (n <= 128) launch_quantize<IO, 32, 4>(p, s);
+    else if (n <= 256) launch_quantize<IO, 256, 1>(p, s);
+    else if (n <= 512) launch_quantize<IO, 256, 2>(p, s);
+    else launch_quantize<IO, 256, 4>(p, s);
+}
+
 sgr_status_t quantize(const QuantParams &p, sgr_dtype_t dtype, cudaStream_t s) {
-    const unsigned grid = unsigned(std::min<int64_t>(p.rows, 148 * 64));
-    if (dtype == SGR_F32) int8_quantize_kernel<float><<<grid, 256, 0, s>>>(p);
-    else if (dtype == SGR_BF16) int8_quantize_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else int8_quantize_kernel<__half><<<grid, 256, 0, s>>>(p);
+    if (dtype == SGR_F32) quantize_rows<float>(p, s);
+    else if (dtype == SGR_BF16) quantize_rows<__nv_bfloat16>(p, s);
+    else quantize_rows<__half>(p, s);
     return cudaGetLastError() == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
 }
 
@@ -62,7 +81,7 @@ cudaError_t launch_split(const ProjectParams &p, int sms, cudaStream_t s) {
     if (!row_map(&map_w, p.w, p.N, p.K, p.w_rs, 128) || !row_map(&map_x, p.x, p.M, p.K, p.x_rs, NT))
         return cudaErrorInvalidValue;
     auto kernel = int8_project_split_kernel<NT, OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::smem_bytes));
+    const cudaError_t e = host::allow_smem<int8_project_split_kernel<NT, OUT>>(int(S::smem_bytes));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(ct * tt * C));
@@ -86,7 +105,7 @@ cudaError_t launch_pair(const ProjectParams &p, int sms, cudaStream_t s) {
     if (!row_map(&map_w, p.w, p.N, p.K, p.w_rs, 128) || !row_map(&map_x, p.x, p.M, p.K, p.x_rs, 128))
         return cudaErrorInvalidValue;
     auto kernel = int8_project_pair_kernel<OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(pair::kSmemBytes));
+    const cudaError_t e = host::allow_smem<int8_project_pair_kernel<OUT>>(int(pair::kSmemBytes));
     if (e != cudaSuccess) return e;
     const unsigned grid = 2 * unsigned(std::min<int64_t>(ct * tt, sms / 2));
     kernel<<<grid, pair::kThreads, pair::kSmemBytes, s>>>(p, int(ct), int(ct * tt), map_w, map_x);

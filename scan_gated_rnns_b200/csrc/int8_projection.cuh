@@ -70,24 +70,104 @@ __device__ __forceinline__ float2 row_scale(float m) {
     return make_float2(s, __fdiv_rn(1.f, s));
 }
 
-template <typename IO>
+// One row per TPR threads of a block of 256, held in registers between the
+// maximum and the rounding: NV vectors of 16 bytes a thread, so the row is
+// read once.  Rows that do not fit (NV = 0) or do not start on 16-byte
+// boundaries are read twice, element by element.
+template <typename IO> __device__ __forceinline__ void unpack16(uint4 x, float (&v)[16 / sizeof(IO)]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(IO) == 4) {
+            v[i] = __uint_as_float(w[i]);
+        } else {
+            const float2 t = Conv<IO, 2>::in(w[i]);
+            v[2 * i] = t.x;
+            v[2 * i + 1] = t.y;
+        }
+    }
+}
+
+template <typename IO, int TPR, int NV>
 __global__ void __launch_bounds__(256) int8_quantize_kernel(const QuantParams p) {
+    constexpr int VEC = 16 / sizeof(IO), ROWS = 256 / TPR;
     __shared__ float s_max[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const typename Raw<IO, 1>::type *x = static_cast<const typename Raw<IO, 1>::type *>(p.x) + row * p.x_rs;
+    const int part = threadIdx.x % TPR;
+    // a block reduction holds a barrier, so every thread of the block stays in the loop
+    for (int64_t row0 = int64_t(blockIdx.x) * ROWS; row0 < p.rows; row0 += int64_t(gridDim.x) * ROWS) {
+        const int64_t row = row0 + threadIdx.x / TPR;
+        const bool on = row < p.rows;
+        const IO *x = static_cast<const IO *>(p.x) + (on ? row : 0) * p.x_rs;
+        using W = typename Raw<IO, 1>::type;
+        float v[NV > 0 ? NV : 1][VEC];
         float m = 0.f;
-        for (int64_t k = threadIdx.x; k < p.K; k += blockDim.x) m = absmax(m, Conv<IO, 1>::in(x[k]));
+        if constexpr (NV > 0) {
+            uint4 raw[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t k = int64_t(i * TPR + part) * VEC;
+                raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (on && k + VEC <= p.K) {
+                    raw[i] = __ldcs(reinterpret_cast<const uint4 *>(x + k));
+                } else if (on && k < p.K) {
+                    for (int j = 0; j < int(p.K - k); ++j) {
+                        const uint32_t e = reinterpret_cast<const W *>(x)[k + j];
+                        const int at = j * int(sizeof(IO));
+                        const uint32_t y = sizeof(IO) == 4 ? e : e << (8 * (at & 3));
+                        if (at < 4) raw[i].x |= y;
+                        else if (at < 8) raw[i].y |= y;
+                        else if (at < 12) raw[i].z |= y;
+                        else raw[i].w |= y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                unpack16<IO>(raw[i], v[i]);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) m = absmax(m, v[i][j]);
+            }
+        } else if (on) {
+            for (int64_t k = part; k < p.K; k += TPR) m = absmax(m, Conv<IO, 1>::in(reinterpret_cast<const W *>(x)[k]));
+        }
+#pragma unroll
         for (int o = 16; o; o >>= 1) m = absmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) s_max[warp] = m;
-        __syncthreads();
-        m = s_max[0];
-        for (int w = 1; w < 8; ++w) m = absmax(m, s_max[w]);
+        if constexpr (TPR > 32) {
+            if (lane == 0) s_max[warp] = m;
+            __syncthreads();
+            m = s_max[0];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) m = absmax(m, s_max[w]);
+            __syncthreads();
+        }
         const float2 s = row_scale(m);
-        if (threadIdx.x == 0) p.scale[row] = s.x;
-        for (int64_t k = threadIdx.x; k < p.K; k += blockDim.x)
-            p.q[row * p.q_rs + k] = s.y == 0.f ? 0 : int8_t(quantize_one(Conv<IO, 1>::in(x[k]), s.x, s.y));
-        __syncthreads();
+        if (!on) continue;
+        if (part == 0) p.scale[row] = s.x;
+        int8_t *q = p.q + row * p.q_rs;
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t k = int64_t(i * TPR + part) * VEC;
+                uint32_t w[VEC / 4];
+#pragma unroll
+                for (int j = 0; j < VEC / 4; ++j) {
+                    w[j] = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        w[j] |= uint32_t(uint8_t(s.y == 0.f ? 0 : quantize_one(v[i][4 * j + b], s.x, s.y))) << (8 * b);
+                }
+                if (k + VEC <= p.K) {
+                    if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(q + k) = make_uint2(w[0], w[1]);
+                    else *reinterpret_cast<uint32_t *>(q + k) = w[0];
+                } else {
+                    for (int j = 0; j < int(p.K - k); ++j) q[k + j] = int8_t(w[j / 4] >> (8 * (j % 4)));
+                }
+            }
+        } else {
+            for (int64_t k = part; k < p.K; k += TPR)
+                q[k] = s.y == 0.f ? int8_t(0) : int8_t(quantize_one(Conv<IO, 1>::in(reinterpret_cast<const W *>(x)[k]), s.x, s.y));
+        }
     }
 }
 

@@ -84,6 +84,29 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
+// Four channels of a token, together where they lie on a boundary of their
+// size and inside the row.
+template <typename OUT>
+__device__ __forceinline__ void put4(const ProjectParams &p, int64_t m, int64_t n, int4 acc, float sx, const float (&sw)[4],
+                                     const float (&b)[4]) {
+    const float y[4] = {fmaf(float(acc.x) * sx, sw[0], b[0]), fmaf(float(acc.y) * sx, sw[1], b[1]),
+                        fmaf(float(acc.z) * sx, sw[2], b[2]), fmaf(float(acc.w) * sx, sw[3], b[3])};
+    using W = typename Raw<OUT, 1>::type;
+    W *at = reinterpret_cast<W *>(p.y) + m * p.y_rs + n;
+    if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(at) & (4 * sizeof(OUT) - 1)) == 0) {
+        if constexpr (sizeof(OUT) == 4) {
+            *reinterpret_cast<float4 *>(at) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            *reinterpret_cast<uint2 *>(at) = make_uint2(Conv<OUT, 2>::out(make_float2(y[0], y[1])),
+                                                        Conv<OUT, 2>::out(make_float2(y[2], y[3])));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) at[i] = Conv<OUT, 1>::out(y[i]);
+    }
+}
+
 // ------------------------------------------------- few tokens: split K
 //
 // One block per tile of 128 channels x NT tokens and per part of K; the C
@@ -220,18 +243,44 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
             asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(map_rank(smem_addr(s_bad), c)));
             bad = bad || x != 0;
         }
-        const int live = int(p.M - tok0 < NT ? p.M - tok0 : NT);    // tokens of the tile
+        // this block's share of the tile's tokens, four channels a thread, four tokens in flight
+        const int live = int(p.M - tok0 < NT ? p.M - tok0 : NT);
         const int lo = rank * live / C, hi = (rank + 1) * live / C;
-        for (int t = lo; t < hi; ++t) {
-            int acc = 0;
-            const uint32_t at = smem_addr(sum + t * 128 + threadIdx.x);
-            for (int c = 0; c < C; ++c) {
-                int x;
-                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(map_rank(at, c)));
-                acc += x;
+        const int64_t n4 = int64_t(ct) * 128 + 4 * lane;
+        float w4[4], b4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w4[i] = n4 + i < p.N ? p.w_scale[n4 + i] : 0.f;
+            b4[i] = n4 + i < p.N && p.bias ? p.bias[n4 + i] : 0.f;
+        }
+        for (int t0 = lo + warp; t0 < hi; t0 += 16) {
+            int4 acc[4];
+            float sx[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                acc[u] = make_int4(0, 0, 0, 0);
+                sx[u] = t0 + 4 * u < hi ? p.x_scale[tok0 + t0 + 4 * u] : 0.f;
+                if (bad) sx[u] = __int_as_float(0x7fffffff);
             }
-            const int64_t m = tok0 + t;
-            if (nvalid) put<OUT>(p, m, n, acc, bad ? __int_as_float(0x7fffffff) : p.x_scale[m], sw, b);
+            for (int c = 0; c < C; ++c) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (t0 + 4 * u < hi) {
+                        int4 x;
+                        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"(map_rank(smem_addr(sum + (t0 + 4 * u) * 128 + 4 * lane), c)));
+                        acc[u].x += x.x;
+                        acc[u].y += x.y;
+                        acc[u].z += x.z;
+                        acc[u].w += x.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (t0 + 4 * u < hi) put4<OUT>(p, tok0 + t0 + 4 * u, n4, acc[u], sx[u], w4, b4);
+            }
         }
         cluster_sync();                                             // a peer may still be reading
     }

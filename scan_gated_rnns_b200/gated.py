@@ -11,6 +11,7 @@ only; every operation runs in ``libsgr.so``):
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -38,12 +39,28 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name}: dtype {t.dtype} is not supported (float32, bfloat16 or float16)") from None
 
 
+# the raw handle of a device's current stream (a step is short beside the
+# objects that the public call builds)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(fn, device: int, *args) -> int:
+    """fn(*args, stream) on `device` and its current stream."""
+    stream = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if device == torch.cuda.current_device():
+        return fn(*args, stream)
+    with torch.cuda.device(device):
+        return fn(*args, stream)
+
+
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Row stride, in elements, of a tensor whose leading dimensions count rows
     that lie evenly spaced, each of them contiguous."""
     shape, stride = t.shape, t.stride()
-    if shape[-1] > 1 and stride[-1] != 1:
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
+    if len(shape) == 2:
+        return stride[0] if shape[0] != 1 else shape[1]
     step, rows = None, 1
     for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
         if n == 1:
@@ -58,7 +75,7 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 
 def _operand(t: torch.Tensor, like: Optional[torch.Tensor], name: str) -> int:
     ops._need_cuda(t, name)
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must match the first operand's shape, dtype and device")
     return _row_stride(t, name)
 
@@ -74,32 +91,40 @@ def _sequences(fn: str, f: torch.Tensor, cu: Optional[torch.Tensor]) -> Tuple[in
     if f.dim() != 2:
         raise ValueError(f"{fn}: with cu_seqlens f must be packed rows (N, D), got shape {tuple(f.shape)}")
     ops._need_cuda(cu, fn + ": cu_seqlens")
-    if cu.dtype not in _INDEX or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous() or cu.device != f.device:
+    if cu.dtype not in _INDEX or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous() or \
+            cu.get_device() != f.get_device():
         raise ValueError(f"{fn}: cu_seqlens must be a contiguous (sequences + 1,) int32 or int64 vector on {f.device}")
     return f.shape[0], f.shape[1], cu.shape[0] - 1, cu.data_ptr(), _INDEX[cu.dtype]
 
 
-def _states(t: Optional[torch.Tensor], n: int, D: int, device, name: str, shared: bool) -> Tuple[int, int]:
-    """(pointer, row stride) of fp32 states (n, D), or (D,) where one may serve all."""
+def _states(t: Optional[torch.Tensor], n: int, D: int, like: torch.Tensor, name: str, shared: bool) -> Tuple[int, int]:
+    """(pointer, row stride) of fp32 states (n, D), or (D,) where one may serve
+    all, on like's device."""
     if t is None:
         return 0, 0
     ops._need_cuda(t, name)
-    if t.dtype != torch.float32 or t.device != device:
-        raise ValueError(f"{name} must be float32 on {device}")
-    if shared and t.dim() == 1:
-        if t.shape[0] != D or (D > 1 and t.stride(0) != 1):
+    if t.dtype is not torch.float32 or t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be float32 on {like.device}")
+    shape, stride = t.shape, t.stride()
+    if shared and len(shape) == 1:
+        if shape[0] != D or (D > 1 and stride[0] != 1):
             raise ValueError(f"{name} must be a contiguous (D,) vector")
         return t.data_ptr(), 0
-    if tuple(t.shape) != (n, D) or (D > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be ({n}, {D}) with contiguous rows, got {tuple(t.shape)}")
-    return t.data_ptr(), (t.stride(0) if n > 1 else D)
+    if len(shape) != 2 or shape[0] != n or shape[1] != D or (D > 1 and stride[1] != 1):
+        raise ValueError(f"{name} must be ({n}, {D}) with contiguous rows, got {tuple(shape)}")
+    return t.data_ptr(), (stride[0] if n > 1 else D)
 
 
-def _scratch(rows: int, D: int, device) -> Tuple[torch.Tensor, int]:
+@functools.lru_cache(maxsize=4096)
+def _sizes(rows: int, D: int) -> Tuple[int, int]:
+    """(bytes of workspace, rows of kept states)."""
+    return int(lib().sgr_gated_workspace_size(rows, D)), int(lib().sgr_gated_chunks(rows))
+
+
+def _scratch(need: int, device) -> Optional[torch.Tensor]:
     """The call's own workspace: of the caching allocator, so that calls on
     other streams and captured graphs each have theirs."""
-    need = int(lib().sgr_gated_workspace_size(rows, D))
-    return torch.empty(max(need, 1), dtype=torch.uint8, device=device), need
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
 def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = None,
@@ -120,19 +145,19 @@ def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = No
     v_rs = _operand(v, f, fn + ": v")
     dt = _dtype_code(f, fn)
     rows, D, n, cp, cb = _sequences(fn, f, cu_seqlens)
-    hp, hss = _states(h0, n, D, f.device, fn + ": h0", True)
+    hp, hss = _states(h0, n, D, f, fn + ": h0", True)
     zero = out is None
-    if out is None:
-        out = torch.empty(f.shape, dtype=f.dtype, device=f.device)
+    device = f.device
+    if zero:
+        out = torch.empty(f.shape, dtype=f.dtype, device=device)
     o_rs = _operand(out, f, fn + ": out")
-    h_last = torch.empty((n, D), dtype=torch.float32, device=f.device)
-    chunks = int(lib().sgr_gated_chunks(rows))
-    states = torch.empty((chunks, D), dtype=torch.float32, device=f.device) if save_states else None
-    with torch.cuda.device(f.device):
-        ws, need = _scratch(rows, D, f.device)
-        code = lib().gated_scan(f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n, out.data_ptr(), o_rs,
-                                h_last.data_ptr(), states.data_ptr() if save_states else 0, rows, D, g, dt, int(zero),
-                                ws.data_ptr(), need, ops._stream(f.device))
+    h_last = torch.empty((n, D), dtype=torch.float32, device=device)
+    need, chunks = _sizes(rows, D)
+    states = torch.empty((chunks, D), dtype=torch.float32, device=device) if save_states else None
+    ws = _scratch(need, device)
+    code = _launch(lib().gated_scan, device.index, f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n,
+                   out.data_ptr(), o_rs, h_last.data_ptr(), states.data_ptr() if save_states else 0, rows, D, g, dt,
+                   int(zero), ws.data_ptr() if need else 0, need)
     check(fn, code)
     return (out, h_last, states) if save_states else (out, h_last)
 
@@ -150,23 +175,22 @@ def gated_scan_backward(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Ten
     dh_rs = _operand(dh, f, fn + ": dh")
     dt = _dtype_code(f, fn)
     rows, D, n, cp, cb = _sequences(fn, f, cu_seqlens)
-    hp, hss = _states(h0, n, D, f.device, fn + ": h0", True)
-    lp, lss = _states(dh_last, n, D, f.device, fn + ": dh_last", False)
+    hp, hss = _states(h0, n, D, f, fn + ": h0", True)
+    lp, lss = _states(dh_last, n, D, f, fn + ": dh_last", False)
     if lp and n > 1 and lss != D:
         raise ValueError(f"{fn}: dh_last must be contiguous")
-    chunks = int(lib().sgr_gated_chunks(rows))
-    sp, sss = _states(states, chunks, D, f.device, fn + ": states", False)
+    need, chunks = _sizes(rows, D)
+    sp, sss = _states(states, chunks, D, f, fn + ": states", False)
     if states is None or (chunks > 1 and sss != D):
         raise ValueError(f"{fn}: states must be the contiguous ({chunks}, {D}) tensor that gated_scan saved")
-    df = torch.empty(f.shape, dtype=f.dtype, device=f.device)
-    dv = torch.empty(f.shape, dtype=f.dtype, device=f.device)
-    dh0 = torch.empty((n, D), dtype=torch.float32, device=f.device) if want_dh0 else None
-    with torch.cuda.device(f.device):
-        ws, need = _scratch(rows, D, f.device)
-        code = lib().gated_scan_backward(f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n, sp, dh.data_ptr(),
-                                         dh_rs, lp, df.data_ptr(), D, dv.data_ptr(), D,
-                                         dh0.data_ptr() if want_dh0 else 0, rows, D, g, dt, ws.data_ptr(), need,
-                                         ops._stream(f.device))
+    device = f.device
+    df = torch.empty(f.shape, dtype=f.dtype, device=device)
+    dv = torch.empty(f.shape, dtype=f.dtype, device=device)
+    dh0 = torch.empty((n, D), dtype=torch.float32, device=device) if want_dh0 else None
+    ws = _scratch(need, device)
+    code = _launch(lib().gated_scan_backward, device.index, f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n, sp,
+                   dh.data_ptr(), dh_rs, lp, df.data_ptr(), D, dv.data_ptr(), D, dh0.data_ptr() if want_dh0 else 0, rows,
+                   D, g, dt, ws.data_ptr() if need else 0, need)
     check(fn, code)
     return df, dv, dh0
 
@@ -223,22 +247,23 @@ def gated_step(f: torch.Tensor, v: torch.Tensor, state: torch.Tensor, slots: Opt
     M, D = f.shape
     if state.dim() != 2 or state.shape[1] != D:
         raise ValueError(f"{fn}: state must be (slots, {D}), got {tuple(state.shape)}")
-    sp, srs = _states(state, state.shape[0], D, f.device, fn + ": state", False)
+    sp, srs = _states(state, state.shape[0], D, f, fn + ": state", False)
     kp = kb = 0
     if slots is not None:
         ops._need_cuda(slots, fn + ": slots")
-        if slots.dtype not in _INDEX or tuple(slots.shape) != (M,) or not slots.is_contiguous() or \
-                slots.device != f.device:
+        if slots.dtype not in _INDEX or slots.dim() != 1 or slots.shape[0] != M or not slots.is_contiguous() or \
+                slots.get_device() != f.get_device():
             raise ValueError(f"{fn}: slots must be a contiguous ({M},) int32 or int64 vector on {f.device}")
         kp, kb = slots.data_ptr(), _INDEX[slots.dtype]
     elif state.shape[0] < M:
         raise ValueError(f"{fn}: state has {state.shape[0]} rows for {M} requests")
     zero = out is None
-    if out is None:
+    if zero:
         out = torch.empty((M, D), dtype=f.dtype, device=f.device)
-    o_rs = _operand(out, f, fn + ": out")
-    with torch.cuda.device(f.device):
-        code = lib().gated_step(f.data_ptr(), f_rs, v.data_ptr(), v_rs, sp, srs, state.shape[0], kp, kb,
-                                out.data_ptr(), o_rs, M, D, g, dt, int(zero), ops._stream(f.device))
+        o_rs = D
+    else:
+        o_rs = _operand(out, f, fn + ": out")
+    code = _launch(lib().gated_step, f.get_device(), f.data_ptr(), f_rs, v.data_ptr(), v_rs, sp, srs, state.shape[0], kp, kb,
+                   out.data_ptr(), o_rs, M, D, g, dt, int(zero))
     check(fn, code)
     return out

@@ -6,13 +6,14 @@ both operations run in ``libsgr.so``):
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
 
 from . import _abi, ops
 from ._abi import check, lib
-from .gated import _DT, _dtype_code, _row_stride
+from .gated import _DT, _dtype_code, _launch, _row_stride
 
 
 def int8_quantize(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -34,19 +35,22 @@ def int8_quantize(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     buf = torch.empty((*lead, pad), dtype=torch.int8, device=x.device)
     q = buf[..., :K]
     scale = torch.empty(lead, dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        code = lib().int8_quantize(x.data_ptr(), x_rs, q.data_ptr(), pad, scale.data_ptr(), rows, K, dt,
-                                   ops._stream(x.device))
+    code = _launch(lib().int8_quantize, x.get_device(), x.data_ptr(), x_rs, q.data_ptr(), pad, scale.data_ptr(), rows, K, dt)
     check(fn, code)
     return q, scale
 
 
-def _vector(t: Optional[torch.Tensor], shape, device, name: str) -> int:
+@functools.lru_cache(maxsize=4096)
+def _workspace(rows: int, K: int, dtype: int) -> int:
+    return int(lib().sgr_int8_workspace_size(rows, K, dtype))
+
+
+def _vector(t: Optional[torch.Tensor], shape, like: torch.Tensor, name: str) -> int:
     if t is None:
         return 0
     ops._need_cuda(t, name)
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous float32 {tuple(shape)} tensor on {device}")
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a contiguous float32 {tuple(shape)} tensor on {like.device}")
     return t.data_ptr()
 
 
@@ -69,7 +73,8 @@ def int8_projection(x: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor, x
     if quantised != (x_scale is not None):
         raise ValueError(f"{fn}: x_scale goes with int8 x, and only with it")
     xdt = _abi.SGR_I8 if quantised else _dtype_code(x, fn + ": x")
-    if w_q.dtype != torch.int8 or w_q.dim() != 2 or w_q.shape[1] != x.shape[-1] or w_q.device != x.device:
+    if w_q.dtype != torch.int8 or w_q.dim() != 2 or w_q.shape[1] != x.shape[-1] or \
+            w_q.get_device() != x.get_device():
         raise ValueError(f"{fn}: w_q must be int8 (N, {x.shape[-1]}) on {x.device}")
     N, K = w_q.shape
     if K < 1:
@@ -78,9 +83,9 @@ def int8_projection(x: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor, x
     rows = lead.numel()
     x_rs = _row_stride(x, fn + ": x")
     w_rs = _row_stride(w_q, fn + ": w_q")
-    sp = _vector(x_scale, lead, x.device, fn + ": x_scale")
-    wp = _vector(w_scale, (N,), x.device, fn + ": w_scale")
-    bp = _vector(bias, (N,), x.device, fn + ": bias")
+    sp = _vector(x_scale, lead, x, fn + ": x_scale")
+    wp = _vector(w_scale, (N,), x, fn + ": w_scale")
+    bp = _vector(bias, (N,), x, fn + ": bias")
     if out is None:
         if out_dtype is None:
             out_dtype = torch.float32 if quantised else x.dtype
@@ -89,14 +94,13 @@ def int8_projection(x: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor, x
         out = torch.empty((*lead, N), dtype=out_dtype, device=x.device)
     else:
         ops._need_cuda(out, fn + ": out")
-        if tuple(out.shape) != (*lead, N) or out.device != x.device or out_dtype not in (None, out.dtype):
+        if tuple(out.shape) != (*lead, N) or out.get_device() != x.get_device() or out_dtype not in (None, out.dtype):
             raise ValueError(f"{fn}: out must be {(*lead, N)} of out_dtype on {x.device}")
     ydt = _dtype_code(out, fn + ": out")
     y_rs = _row_stride(out, fn + ": out")
-    with torch.cuda.device(x.device):
-        need = int(lib().sgr_int8_workspace_size(rows, K, xdt))
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        code = lib().int8_projection(x.data_ptr(), x_rs, xdt, sp, w_q.data_ptr(), w_rs, wp, bp, out.data_ptr(), y_rs,
-                                     ydt, rows, K, N, ws.data_ptr() if need else 0, need, ops._stream(x.device))
+    need = 0 if quantised else _workspace(rows, K, xdt)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    code = _launch(lib().int8_projection, x.get_device(), x.data_ptr(), x_rs, xdt, sp, w_q.data_ptr(), w_rs, wp, bp,
+                   out.data_ptr(), y_rs, ydt, rows, K, N, ws.data_ptr() if need else 0, need)
     check(fn, code)
     return out
