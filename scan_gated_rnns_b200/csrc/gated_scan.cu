@@ -203,10 +203,16 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
                : SGR_ERR_CUDA;
 }
 
-template <typename IO, int V>
+template <typename IO, int V, int U>
 void launch_step(const StepParams &p, int gate, unsigned grid, cudaStream_t s) {
-    if (gate == SGR_GATE_SIGMOID) gated_step_kernel<IO, GATE_SIGMOID, V><<<grid, 256, 0, s>>>(p);
-    else gated_step_kernel<IO, GATE_LOG, V><<<grid, 256, 0, s>>>(p);
+    if (gate == SGR_GATE_SIGMOID) gated_step_kernel<IO, GATE_SIGMOID, V, U><<<grid, 256, 0, s>>>(p);
+    else gated_step_kernel<IO, GATE_LOG, V, U><<<grid, 256, 0, s>>>(p);
+}
+template <typename IO>
+void launch_step_any(const StepParams &p, int gate, int V, int U, unsigned grid, cudaStream_t s) {
+    if (V == 1) launch_step<IO, 1, 1>(p, gate, grid, s);
+    else if (U == 1) launch_step<IO, 4, 1>(p, gate, grid, s);
+    else launch_step<IO, 4, 4>(p, gate, grid, s);
 }
 
 }  // namespace
@@ -281,17 +287,15 @@ sgr_status_t gated_step(const void *f, int64_t f_row_stride, const void *v, int6
     const bool four = strides % 4 == 0 && host::aligned(f, 4 * esz) && host::aligned(v, 4 * esz) &&
                       host::aligned(h, 4 * esz) && host::aligned(state, 16);
     const int V = four ? 4 : 1;
-    p.d_blocks = (D + 256 * V - 1) / (256 * V);
+    // four vectors a thread once one each would give every SM more than two blocks
+    const int64_t one = (D + 256 * V - 1) / (256 * V);
+    const int U = four && one >= 4 && rows * one > 2 * 148 ? 4 : 1;
+    p.d_blocks = (one + U - 1) / U;
     int64_t grid = 0;
     if (!host::mul_ok(rows, p.d_blocks, &grid) || grid > std::numeric_limits<int>::max()) return SGR_ERR_UNSUPPORTED;
-    if (dtype == SGR_F32) {
-        four ? launch_step<float, 4>(p, gate, unsigned(grid), stream) : launch_step<float, 1>(p, gate, unsigned(grid), stream);
-    } else if (dtype == SGR_BF16) {
-        four ? launch_step<__nv_bfloat16, 4>(p, gate, unsigned(grid), stream)
-             : launch_step<__nv_bfloat16, 1>(p, gate, unsigned(grid), stream);
-    } else {
-        four ? launch_step<__half, 4>(p, gate, unsigned(grid), stream) : launch_step<__half, 1>(p, gate, unsigned(grid), stream);
-    }
+    if (dtype == SGR_F32) launch_step_any<float>(p, gate, V, U, unsigned(grid), stream);
+    else if (dtype == SGR_BF16) launch_step_any<__nv_bfloat16>(p, gate, V, U, unsigned(grid), stream);
+    else launch_step_any<__half>(p, gate, V, U, unsigned(grid), stream);
     return cudaGetLastError() == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
 }
 

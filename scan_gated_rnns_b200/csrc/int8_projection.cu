@@ -28,18 +28,22 @@ void launch_quantize(const QuantParams &p, cudaStream_t s) {
     const int64_t blocks = (p.rows + 256 / TPR - 1) / (256 / TPR);
     int8_quantize_kernel<IO, TPR, NV><<<unsigned(std::min<int64_t>(blocks, 148 * 32)), 256, 0, s>>>(p);
 }
-// A warp per row up to 4 vectors a lane, a block up to 4 a thread (bf16: rows of 1024 and 8192 values).
+// Up to 4 vectors a thread: a warp a row (bf16: 1024 values), four warps
+// (4096), a block (8192).  Fewer rows than SMs take a block each up to there,
+// for the latency.
 template <typename IO>
 void quantize_rows(const QuantParams &p, cudaStream_t s) {
     constexpr int VEC = 16 / sizeof(IO);
     const bool vec = host::aligned(p.x, 16) && host::aligned(p.q, 16) &&
                      (p.rows <= 1 || (p.x_rs * int64_t(sizeof(IO)) % 16 == 0 && p.q_rs % 16 == 0));
     const int64_t n = (p.K + VEC - 1) / VEC;
+    const bool few = p.rows <= 148;
     if (!vec || n > 4 * 256) launch_quantize<IO, 256, 0>(p, s);
     else if (n <= 32) launch_quantize<IO, 32, 1>(p, s);
-    else if (n <= 128) launch_quantize<IO, 32, 4>(p, s);
-    else if (n <= 256) launch_quantize<IO, 256, 1>(p, s);
-    else if (n <= 512) launch_quantize<IO, 256, 2>(p, s);
+    else if (n <= 128 && !few) launch_quantize<IO, 32, 4>(p, s);
+    else if (n <= 256 && few) launch_quantize<IO, 256, 1>(p, s);
+    else if (n <= 512 && few) launch_quantize<IO, 256, 2>(p, s);
+    else if (n <= 512) launch_quantize<IO, 128, 4>(p, s);
     else launch_quantize<IO, 256, 4>(p, s);
 }
 

@@ -47,6 +47,37 @@ __device__ __forceinline__ int quantize_one(float x, float s, float inv) {
     return int(q);
 }
 
+// N values at once: t = x (1 / s) + 3 2^22 leaves a whole number in its low
+// bits.  x (1 / s) is off from the quotient by at most 127 2^-23 (the hardware's
+// 1 / s), so where it is more than 2^-15 away from a half the whole number is
+// right; a group with a quotient nearer to one (one in two thousand) is
+// decided exactly.  Packs four to a word.
+template <int N>
+__device__ __forceinline__ void quantize_words(const float2 (&x)[N / 2], float s, float inv, uint32_t (&w)[N / 4]) {
+    const float2 i2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f), minus = make_float2(-1.f, -1.f);
+    float2 t[N / 2];
+    float far = 0.f;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        t[i] = __ffma2_rn(x[i], i2, magic);
+        const float2 d = __ffma2_rn(x[i], i2, __ffma2_rn(t[i], minus, magic));
+        far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+    }
+    if (far > 0.5f - 1.f / 32768.f) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 v = x[i];
+            t[i] = make_float2(__int_as_float(quantize_one(v.x, s, inv)), __int_as_float(quantize_one(v.y, s, inv)));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const uint32_t lo = __byte_perm(__float_as_uint(t[2 * i].x), __float_as_uint(t[2 * i].y), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(t[2 * i + 1].x), __float_as_uint(t[2 * i + 1].y), 0x0040);
+        w[i] = __byte_perm(lo, hi, 0x5410);
+    }
+}
+
 struct QuantParams {
     const void *x;
     int64_t x_rs;                  // elements
@@ -56,54 +87,75 @@ struct QuantParams {
     int64_t rows, K;
 };
 
-// largest |x| of a row: NaN where one is NaN
-__device__ __forceinline__ float absmax(float m, float x) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
-    return r;
-}
-
-// (scale, 1 / scale) of a row whose largest |x| is m
+// (scale, 1 / scale) of a row whose largest |x| is m.  m / 127 is rounded
+// correctly by one step from the product with the rounded reciprocal
+// (Markstein, 1990): the remainder m - 127 q is exact in an fma.  The second
+// value, the hardware's reciprocal, is 0 for a row that is not finite.
 __device__ __forceinline__ float2 row_scale(float m) {
     if (!(m <= 3.402823466e38f)) return make_float2(__int_as_float(0x7fffffff), 0.f);
-    const float s = fmaxf(__fdiv_rn(m, 127.f), kScaleFloor);
-    return make_float2(s, __fdiv_rn(1.f, s));
+    constexpr float r = 1.f / 127.f;
+    const float q = m * r;
+    const float s = fmaxf(fmaf(fmaf(-127.f, q, m), r, q), kScaleFloor);
+    return make_float2(s, fast_rcp(s));
 }
 
 // One row per TPR threads of a block of 256, held in registers between the
 // maximum and the rounding: NV vectors of 16 bytes a thread, so the row is
 // read once.  Rows that do not fit (NV = 0) or do not start on 16-byte
-// boundaries are read twice, element by element.
-template <typename IO> __device__ __forceinline__ void unpack16(uint4 x, float (&v)[16 / sizeof(IO)]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(IO) == 4) {
-            v[i] = __uint_as_float(w[i]);
-        } else {
-            const float2 t = Conv<IO, 2>::in(w[i]);
-            v[2 * i] = t.x;
-            v[2 * i + 1] = t.y;
-        }
+// boundaries are read twice, element by element.  Short rows take a warp
+// each, longer ones the block, of which an SM holds six or more: a row's
+// barrier passes under the others' loads (8192 rows of 4096 bf16; a warp a
+// row, 16 vectors a lane, needed 245 registers and 117 us).
+template <typename IO> __device__ __forceinline__ void unpack16(const uint4 &x, float2 (&v)[8 / sizeof(IO)]) {
+    if constexpr (sizeof(IO) == 4) {
+        v[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+        v[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+    } else {
+        v[0] = Conv<IO, 2>::in(x.x);
+        v[1] = Conv<IO, 2>::in(x.y);
+        v[2] = Conv<IO, 2>::in(x.z);
+        v[3] = Conv<IO, 2>::in(x.w);
     }
+}
+// Largest |x| as bits: magnitudes of one type order as whole numbers do, NaN
+// above all.  16-bit types two at a time, the halves joined at the end.
+template <typename H2> __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+    const H2 m = __hmax2_nan(*reinterpret_cast<const H2 *>(&a), __habs2(*reinterpret_cast<const H2 *>(&b)));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+template <typename IO> __device__ __forceinline__ uint32_t max_bits(uint32_t m, const uint4 &x) {
+    if constexpr (sizeof(IO) == 4) {
+        const uint32_t k = 0x7fffffffu;
+        return max(max(max(m, x.x & k), max(x.y & k, x.z & k)), x.w & k);
+    } else {
+        using H2 = typename std::conditional<std::is_same<IO, __half>::value, __half2, __nv_bfloat162>::type;
+        return max_pair<H2>(max_pair<H2>(max_pair<H2>(max_pair<H2>(m, x.x), x.y), x.z), x.w);
+    }
+}
+template <typename IO> __device__ __forceinline__ uint32_t join_bits(uint32_t m) {
+    return sizeof(IO) == 4 ? m : max(m & 0xffffu, m >> 16);
+}
+template <typename IO> __device__ __forceinline__ float max_value(uint32_t m) {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(m);
+    else return Conv<IO, 1>::in(uint16_t(m));
 }
 
 template <typename IO, int TPR, int NV>
-__global__ void __launch_bounds__(256) int8_quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(256, NV >= 4 ? 4 : 6) int8_quantize_kernel(const QuantParams p) {
     constexpr int VEC = 16 / sizeof(IO), ROWS = 256 / TPR;
-    __shared__ float s_max[8];
+    __shared__ uint32_t s_max[2][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int turn = 0;
     const int part = threadIdx.x % TPR;
+    using W = typename Raw<IO, 1>::type;
     // a block reduction holds a barrier, so every thread of the block stays in the loop
     for (int64_t row0 = int64_t(blockIdx.x) * ROWS; row0 < p.rows; row0 += int64_t(gridDim.x) * ROWS) {
         const int64_t row = row0 + threadIdx.x / TPR;
         const bool on = row < p.rows;
         const IO *x = static_cast<const IO *>(p.x) + (on ? row : 0) * p.x_rs;
-        using W = typename Raw<IO, 1>::type;
-        float v[NV > 0 ? NV : 1][VEC];
-        float m = 0.f;
+        uint4 raw[NV > 0 ? NV : 1];
+        uint32_t bits = 0;
         if constexpr (NV > 0) {
-            uint4 raw[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t k = int64_t(i * TPR + part) * VEC;
@@ -123,25 +175,21 @@ __global__ void __launch_bounds__(256) int8_quantize_kernel(const QuantParams p)
                 }
             }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                unpack16<IO>(raw[i], v[i]);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) m = absmax(m, v[i][j]);
-            }
+            for (int i = 0; i < NV; ++i) bits = max_bits<IO>(bits, raw[i]);
+            bits = join_bits<IO>(bits);
         } else if (on) {
-            for (int64_t k = part; k < p.K; k += TPR) m = absmax(m, Conv<IO, 1>::in(reinterpret_cast<const W *>(x)[k]));
+            for (int64_t k = part; k < p.K; k += TPR)
+                bits = max(bits, uint32_t(reinterpret_cast<const W *>(x)[k]) & (sizeof(IO) == 4 ? 0x7fffffffu : 0x7fffu));
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = absmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+        bits = __reduce_max_sync(0xffffffffu, bits);
         if constexpr (TPR > 32) {
-            if (lane == 0) s_max[warp] = m;
-            __syncthreads();
-            m = s_max[0];
-#pragma unroll
-            for (int w = 1; w < 8; ++w) m = absmax(m, s_max[w]);
-            __syncthreads();
+            constexpr int PER = TPR / 32;                  // warps of a row
+            if (lane == 0) s_max[turn][warp] = bits;
+            __syncthreads();                               // one a row: the next writes the other half
+            bits = __reduce_max_sync(0xffffffffu, s_max[turn][warp / PER * PER + lane % PER]);
+            turn ^= 1;
         }
-        const float2 s = row_scale(m);
+        const float2 s = row_scale(max_value<IO>(bits));
         if (!on) continue;
         if (part == 0) p.scale[row] = s.x;
         int8_t *q = p.q + row * p.q_rs;
@@ -149,13 +197,11 @@ __global__ void __launch_bounds__(256) int8_quantize_kernel(const QuantParams p)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t k = int64_t(i * TPR + part) * VEC;
-                uint32_t w[VEC / 4];
-#pragma unroll
-                for (int j = 0; j < VEC / 4; ++j) {
-                    w[j] = 0;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        w[j] |= uint32_t(uint8_t(s.y == 0.f ? 0 : quantize_one(v[i][4 * j + b], s.x, s.y))) << (8 * b);
+                uint32_t w[VEC / 4] = {};
+                if (s.y != 0.f) {
+                    float2 v[VEC / 2];
+                    unpack16<IO>(raw[i], v);
+                    quantize_words<VEC>(v, s.x, s.y, w);
                 }
                 if (k + VEC <= p.K) {
                     if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(q + k) = make_uint2(w[0], w[1]);

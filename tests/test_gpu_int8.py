@@ -57,6 +57,18 @@ def test_quantize_ties_zeros_and_odd_rows():
     assert bool((q[1:] == 0).all()) and int(q[0].abs().max()) == 127
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_scales_of_many_magnitudes(dtype):
+    """|x| / 127 rounded correctly, over all exponents; q is then 127 or -127."""
+    rng = np.random.default_rng(5)
+    x = rng.normal(size=300000) * np.exp2(rng.integers(-120, 120, 300000).astype(np.float64) * (0.1 if dtype == F16 else 1))
+    x = torch.from_numpy(x).to(dtype)[:, None]
+    q, s = sgr.int8_quantize(x.to(DEV))
+    wq, ws = quantize64(x.double().numpy())
+    assert np.array_equal(s.cpu().numpy(), ws, equal_nan=True)
+    assert np.array_equal(q.cpu().numpy().astype(np.int64), wq)
+
+
 def test_quantize_layouts():
     rng = np.random.default_rng(3)
     x = torch.from_numpy(rng.normal(size=(4, 6, 50))).to(BF16).to(DEV)
