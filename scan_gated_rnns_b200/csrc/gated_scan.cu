@@ -77,7 +77,7 @@ bool mappable(const void *base, int64_t rows, int64_t D, int64_t rs, int esz) {
 }
 
 template <typename IO, int E, int GATE, bool TMA>
-cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
+cudaError_t launch(GatedParams p, bool backward, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -87,6 +87,8 @@ cudaError_t launch(const GatedParams &p, bool backward, cudaStream_t s) {
     const int64_t chunks = (p.rows + tr - 1) / tr;
     const int64_t tiles = p.n_strips * (chunks + p.n_segs - 1);
     const unsigned grid = unsigned(std::max<int64_t>(1, p.ticket ? std::min<int64_t>(tiles, sms) : tiles));
+    const int64_t held = int64_t(grid) * (backward ? kBwdSlots : kSlots);
+    p.window = int(std::min<int64_t>(kNear + 32, held / (p.n_strips * p.n_segs) + 2));
     CUtensorMap m[3];
     std::memset(m, 0, sizeof(m));
     if (TMA) {

@@ -87,6 +87,7 @@ struct GatedParams {
     uint32_t *ticket;                      // ~0 at launch, or null: one chunk, tile = blockIdx.x
     uint32_t *status;                      // ~0 at launch; SGR_ERR_TIMEOUT once a wait ran out; may be null
     uint32_t spin_limit;
+    int window;                            // chunks of a strip and segment that blocks may hold at a time
 };
 
 // bound i, clamped to what rows can be
@@ -253,10 +254,12 @@ template <int E> __device__ __forceinline__ void apply_words(const uint64_t (&m)
 // waits, and returns the entering states.  Tiles whose first row (in
 // processing order) is a start enter with 0, which they never use.  One round
 // trip reads the words of the kNear tiles before for every channel, and those
-// of 32 more for the strip's first channel: as a rule the state is among the
-// near ones (wide rows: few tiles of a strip are in flight), else a second
-// round trip reads the rest of the channels.  `meanwhile` runs under the
-// first.
+// of up to 32 more for the strip's first channel; if the state is among the
+// far ones, a second round trip reads the rest of the channels.  No word is
+// read that lies further back than the blocks can hold tiles of the strip
+// (p.window), and where those are few the first round reads the tile before
+// alone: an older word has left L2 for memory, and a load from there, behind
+// the streams, took 2.7 us.  `meanwhile` runs under the first round.
 constexpr int kNear = 4;
 template <int E, class Meanwhile>
 __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int q, int word, bool last, int lane,
@@ -287,9 +290,10 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
     for (uint32_t polls = 0; !found; ++polls) {
         uint64_t m[kNear][E];
         uint32_t st[kNear][E];
+        const int reach = polls == 0 && p.window <= 8 ? 1 : (q < p.window ? q : p.window);
 #pragma unroll
         for (int i = 0; i < kNear; ++i) {
-            if (q - 1 - i >= 0) {
+            if (i < reach) {
                 load_states<E>(p.carry + at - (i + 1) * step, st[i]);
                 load_maps<E>(p.maps + at - (i + 1) * step, m[i]);
             } else {
@@ -300,7 +304,7 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
         const int far = 1 + kNear + lane;                          // this lane probes the tile that far before
         uint32_t ps = kNone;
         uint64_t pm = ~uint64_t(0);
-        if (q - far >= 0) {
+        if (far <= reach) {
             ps = ld_relaxed_u32(p.carry + (word - far) * step + strip * TC);
             pm = ld_relaxed_u64(p.maps + (word - far) * step + strip * TC);
         }
