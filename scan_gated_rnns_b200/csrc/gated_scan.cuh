@@ -536,6 +536,15 @@ template <int TR> struct Segments {
     }
 };
 
+// A tile load that says its lines will not be wanted again, so that the words
+// that blocks hand one another stay in L2.
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+}
+
 // The feeding warp: draws tickets, starts the copies of a tile when its slot
 // is free, writes its table and hands both over.  `reverse`: places count
 // from the segment's end.  Ends with one entry for each carry warp that says
@@ -558,6 +567,8 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
     __syncwarp();
     Segments<TR> seg;
     seg.init(p, bounds, lane);
+    uint64_t once;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     int ends = 0;
     for (int n = 0; ends < kCarryWarps; ++n) {
         const uint32_t tile = __shfl_sync(0xffffffffu, ticket, 0);
@@ -582,9 +593,9 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(OPS * OP_BYTES)
                                  : "memory");
-                    tma_load_2d(dst, m0, int(strip) * TC, int(row0), bar);
-                    tma_load_2d(dst + OP_BYTES, m1, int(strip) * TC, int(row0), bar);
-                    if constexpr (OPS == 3) tma_load_2d(dst + 2 * OP_BYTES, m2, int(strip) * TC, int(row0), bar);
+                    load_tile(dst, m0, int(strip) * TC, int(row0), bar, once);
+                    load_tile(dst + OP_BYTES, m1, int(strip) * TC, int(row0), bar, once);
+                    if constexpr (OPS == 3) load_tile(dst + 2 * OP_BYTES, m2, int(strip) * TC, int(row0), bar, once);
                 }
                 ticket = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : uint32_t(p.n_strips);
                 info.row0 = row0;
@@ -956,30 +967,37 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             const auto v = reader<IO, E, TMA, R, Shape, 1>(p, smem, n % S, warp, lane, row, d0, p.v, p.v_rs);
             const auto dh = reader<IO, E, TMA, R, Shape, 2>(p, smem, n % S, warp, lane, row, d0, p.dh, p.dh_rs);
             const uint4 k = info.masks[warp];
-            V a[R];
-            V A = vset<V>(1.f), B = vset<V>(0.f);
+            V A = vset<V>(1.f), B = vset<V>(0.f), RA = vset<V>(1.f), RB = vset<V>(0.f);
+            // a tile inside one sequence takes the rows without a branch, so that their
+            // loads and gates run side by side (with one a row: 148 us for this pass
+            // on bf16 16384 x 2048)
+            auto rows = [&](auto plain) {
+                constexpr bool PLAIN = decltype(plain)::value;
+                V a[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                V z;
-                s[r] = bwd_gate<GATE, IO>(f(r));
-                bwd_split<GATE>(s[r], a[r], z);
-                if (k.x >> r & 1u) {
-                    A = vset<V>(-0.f);
-                    B = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
+                for (int r = 0; r < R; ++r) {
+                    V z;
+                    s[r] = bwd_gate<GATE, IO>(f(r));
+                    bwd_split<GATE>(s[r], a[r], z);
+                    if (!PLAIN && (k.x >> r & 1u)) {
+                        A = vset<V>(-0.f);
+                        B = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
+                    }
+                    B = vfma(a[r], B, GATE == GATE_SIGMOID ? vmul(z, v(r)) : v(r));
+                    A = vmul(A, a[r]);
                 }
-                B = vfma(a[r], B, GATE == GATE_SIGMOID ? vmul(z, v(r)) : v(r));
-                A = vmul(A, a[r]);
-            }
-            V RA = vset<V>(1.f), RB = vset<V>(0.f);
 #pragma unroll
-            for (int r = R - 1; r >= 0; --r) {
-                if (k.y >> r & 1u) {
-                    RA = vset<V>(-0.f);
-                    RB = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
+                for (int r = R - 1; r >= 0; --r) {
+                    if (!PLAIN && (k.y >> r & 1u)) {
+                        RA = vset<V>(-0.f);
+                        RB = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
+                    }
+                    RB = vmul(a[r], vadd(RB, dh(r)));
+                    RA = vmul(RA, a[r]);
                 }
-                RB = vmul(a[r], vadd(RB, dh(r)));
-                RA = vmul(RA, a[r]);
-            }
+            };
+            if (k.w) rows(std::true_type{});
+            else rows(std::false_type{});
             if (!got) A = B = RA = RB = vset<V>(nan_value());
             blk.A[0][n % kQ][warp][lane] = RA;
             blk.B[0][n % kQ][warp][lane] = RB;
@@ -999,20 +1017,25 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             const bool got = wait(&blk.in[n % kQ], n / kQ);
             V h = blk.A[1][n % kQ][warp][lane];
             V c[R];                                                   // df = c g
+            auto forward = [&](auto plain) {
+                constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (k.x >> r & 1u) h = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
-                const V x = v(r);
-                V a, z;
-                bwd_split<GATE>(s[r], a, z);
-                if constexpr (GATE == GATE_SIGMOID) {
-                    c[r] = vmul(vmul(a, z), vfma(x, vset<V>(-1.f), h));
-                    h = vfma(a, h, vmul(z, x));
-                } else {
-                    c[r] = vmap(s[r], h, [](float y, float w) { return is_cut(y) ? 0.f : y * w; });
-                    h = vfma(a, h, x);
+                for (int r = 0; r < R; ++r) {
+                    if (!PLAIN && (k.x >> r & 1u)) h = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
+                    const V x = v(r);
+                    V a, z;
+                    bwd_split<GATE>(s[r], a, z);
+                    if constexpr (GATE == GATE_SIGMOID) {
+                        c[r] = vmul(vmul(a, z), vfma(x, vset<V>(-1.f), h));
+                        h = vfma(a, h, vmul(z, x));
+                    } else {
+                        c[r] = vmap(s[r], h, [](float y, float w) { return is_cut(y) ? 0.f : y * w; });
+                        h = vfma(a, h, x);
+                    }
                 }
-            }
+            };
+            if (k.w) forward(std::true_type{});
+            else forward(std::false_type{});
             V flow = got ? entering<kWarps - 1>(blk, n % kQ, warp, lane, blk.enter[n % kQ][lane]) : vset<V>(nan_value());
             char *pf = static_cast<char *>(p.df) + ((row + R - 1) * p.df_rs + d0) * int64_t(sizeof(IO));
             char *pv = static_cast<char *>(p.dv) + ((row + R - 1) * p.dv_rs + d0) * int64_t(sizeof(IO));
