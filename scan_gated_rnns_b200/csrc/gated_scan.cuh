@@ -884,13 +884,15 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
             __syncwarp();
             if (lane == 0) arrive(&blk.empty[n % S]);
         };
-        for (int n = 0;; n += 2) {
-            const bool even = fold(n, gate[0]);
+        // one copy of either body: with two, for registers that need not move, the warps
+        // spent a fifth of their time waiting for instructions
+#pragma unroll 1
+        for (int n = 0;; ++n) {
+            const bool more = fold(n, gate[0]);
             if (n > 0) replay(n - 1, gate[1]);
-            if (!even) break;
-            const bool odd = fold(n + 1, gate[1]);
-            replay(n, gate[0]);
-            if (!odd) break;
+            if (!more) break;
+#pragma unroll
+            for (int r = 0; r < R; ++r) gate[1][r] = gate[0][r];
         }
     } else if (warp < kWarps + kCarryWarps) {
         carry_loop<E, S, kTR, 1>(p, blk, warp - kWarps, lane);
@@ -1075,13 +1077,15 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             __syncwarp();
             if (lane == 0) arrive(&blk.empty[n % S]);
         };
-        for (int n = 0;; n += 2) {
-            const bool even = fold(n, gate[0]);
+        // one copy of either body: with two, for registers that need not move, the warps
+        // spent a fifth of their time waiting for instructions
+#pragma unroll 1
+        for (int n = 0;; ++n) {
+            const bool more = fold(n, gate[0]);
             if (n > 0) replay(n - 1, gate[1]);
-            if (!even) break;
-            const bool odd = fold(n + 1, gate[1]);
-            replay(n, gate[0]);
-            if (!odd) break;
+            if (!more) break;
+#pragma unroll
+            for (int r = 0; r < R; ++r) gate[1][r] = gate[0][r];
         }
     } else if (warp < kWarps + kCarryWarps) {
         carry_loop<E, S, kBwdTR, -1>(p, blk, warp - kWarps, lane);
