@@ -27,16 +27,14 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // come on top of the rows' own.
 struct Layout {
     int64_t n_strips, n_chunks, n_tiles;
-    size_t maps, carry, total;
+    size_t total;
 };
 Layout layout(int64_t rows, int64_t D, int tc, int tr, int segs) {
     Layout l;
     l.n_strips = (D + tc - 1) / tc;
     l.n_chunks = rows <= tr ? 1 : (rows + tr - 1) / tr + segs - 1;
     l.n_tiles = l.n_strips * l.n_chunks;
-    l.maps = kHeader;
-    l.carry = l.maps + size_t(l.n_tiles) * tc * 8;
-    l.total = align_up(l.carry + size_t(l.n_tiles) * tc * 4, 256);
+    l.total = kHeader + size_t(l.n_tiles) * tc * 8;
     return l;
 }
 
@@ -195,10 +193,9 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
         char *w = static_cast<char *>(ws);
         p.status = reinterpret_cast<uint32_t *>(w);
         p.ticket = reinterpret_cast<uint32_t *>(w + kTicketAt);
-        p.maps = reinterpret_cast<uint64_t *>(w + l.maps);
-        p.carry = reinterpret_cast<uint32_t *>(w + l.carry);
+        p.words = reinterpret_cast<uint64_t *>(w + kHeader);
         // nothing of an earlier call is read
-        if (cudaMemsetAsync(w, 0xff, l.carry + size_t(l.n_tiles) * 32 * E * 4, stream) != cudaSuccess) return SGR_ERR_CUDA;
+        if (cudaMemsetAsync(w, 0xff, l.total, stream) != cudaSuccess) return SGR_ERR_CUDA;
     }
     return launch_any(p, dtype, gate == SGR_GATE_LOG ? GATE_LOG : GATE_SIGMOID, E, backward, stream) == cudaSuccess
                ? SGR_OK

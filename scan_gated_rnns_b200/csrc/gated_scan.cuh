@@ -24,9 +24,9 @@
 // and the segments are worked on side by side, so that a tile's predecessor is
 // a round of blocks older (one segment: 64 strips of bf16 32768 x 4096 in 23
 // sequences waited 2.6 us a tile, half of that for the predecessor's own
-// fold).  A map is one 64-bit word, a state one
-// 32-bit word per channel, all of them ~0 before the launch and valid once
-// they are not (arithmetic never gives that NaN), so a look-back is one round
+// fold).  A map, and then in its place the
+// state, is one 64-bit word per channel, ~0 before the launch and valid once
+// it is not (arithmetic never gives that NaN), so a look-back is one round
 // trip to L2, without flags or fences.  Blocks take tiles by ticket in the
 // order they run, so a wait is always for a tile that a running block holds;
 // waits are bounded.
@@ -62,7 +62,7 @@ constexpr int kQ = 2;                      // tiles between fold and the end of 
 constexpr uint32_t kTileWait = 1u << 16;   // polls of a wait inside the block (each suspends for tens of us)
 static_assert(kTR == 2 * kBwdTR, "a forward tile holds two saved states");
 constexpr int kSegs = 32;                  // most segments: one per lane of the feeding warp
-constexpr uint32_t kNone = 0xffffffffu;    // a word not yet published
+constexpr uint64_t kNone = ~uint64_t(0);    // a word not yet published
 
 struct GatedParams {
     const void *f, *v, *dh;                // (rows, D), unit stride along D
@@ -82,8 +82,7 @@ struct GatedParams {
     int64_t n_strips;
     int n_segs;                            // at most kSegs
     int zero_padding;                      // outputs of rows in no sequence: 0 written, else left
-    uint64_t *maps;                        // [tiles][TC] words (A, B), ~0 at launch
-    uint32_t *carry;                       // [tiles][TC] words: state leaving each tile, ~0 at launch
+    uint64_t *words;                       // [chunks][n_strips][TC] what tiles hand on, ~0 at launch
     uint32_t *ticket;                      // ~0 at launch, or null: one chunk, tile = blockIdx.x
     uint32_t *status;                      // ~0 at launch; SGR_ERR_TIMEOUT once a wait ran out; may be null
     uint32_t spin_limit;
@@ -206,60 +205,50 @@ __device__ __forceinline__ void fill_info(const GatedParams &p, const Bounds &cu
     if (lane == 0) t.cut = cut;
 }
 
-__device__ __forceinline__ uint32_t ld_relaxed_u32(const uint32_t *p) {
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
+// A tile's word for a channel: its map (A, B), and later the state behind it,
+// which is the map that cuts, (-0, state).
+__device__ __forceinline__ uint64_t word_of(float A, float B) {
+    return (uint64_t(__float_as_uint(B)) << 32) | __float_as_uint(A);
 }
-__device__ __forceinline__ void st_relaxed_u32(uint32_t *p, uint32_t v) {
-    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint64_t pack_map(float2 m) {
-    return (uint64_t(__float_as_uint(m.y)) << 32) | __float_as_uint(m.x);
-}
+__device__ __forceinline__ float word_a(uint64_t w) { return __uint_as_float(uint32_t(w)); }
+__device__ __forceinline__ float word_b(uint64_t w) { return __uint_as_float(uint32_t(w >> 32)); }
 
 // The words of this lane's E channels: each is read whole.
-template <int E> __device__ __forceinline__ void load_maps(const uint64_t *p, uint64_t (&m)[E]) {
+template <int E> __device__ __forceinline__ void load_words(const uint64_t *p, uint64_t (&m)[E]) {
     if constexpr (E == 1) {
         m[0] = ld_relaxed_u64(p);
     } else {
         asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(m[0]), "=l"(m[1]) : "l"(p) : "memory");
     }
 }
-template <int E> __device__ __forceinline__ void load_states(const uint32_t *p, uint32_t (&s)[E]) {
-    if constexpr (E == 1) {
-        s[0] = ld_relaxed_u32(p);
-    } else {
-        asm volatile("ld.relaxed.gpu.global.v2.u32 {%0, %1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "l"(p) : "memory");
-    }
-}
 template <int E> __device__ __forceinline__ bool words_in(const uint64_t (&m)[E]) {
-    bool ok = m[0] != ~uint64_t(0);
-    if constexpr (E == 2) ok = ok && m[1] != ~uint64_t(0);
+    bool ok = m[0] != kNone;
+    if constexpr (E == 2) ok = ok && m[1] != kNone;
     return ok;
 }
-template <int E> __device__ __forceinline__ bool words_in(const uint32_t (&s)[E]) {
-    bool ok = s[0] != kNone;
-    if constexpr (E == 2) ok = ok && s[1] != kNone;
+// they are states (of words that are in)
+template <int E> __device__ __forceinline__ bool words_cut(const uint64_t (&m)[E]) {
+    bool ok = is_cut(word_a(m[0]));
+    if constexpr (E == 2) ok = ok && is_cut(word_a(m[1]));
     return ok;
 }
 template <int E> __device__ __forceinline__ void apply_words(const uint64_t (&m)[E], float (&h)[E]) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        h[e] = apply_map(__uint_as_float(uint32_t(m[e])), __uint_as_float(uint32_t(m[e] >> 32)), h[e]);
+    for (int e = 0; e < E; ++e) h[e] = apply_map(word_a(m[e]), word_b(m[e]), h[e]);
 }
 
 // The carry of one tile (carry warp): q its place in processing order within
-// its segment, word that of its words, tot the tile's maps of this lane's E channels.  Publishes,
-// waits, and returns the entering states.  Tiles whose first row (in
-// processing order) is a start enter with 0, which they never use.  One round
-// trip reads the words of the kNear tiles before for every channel, and those
-// of up to 32 more for the strip's first channel; if the state is among the
-// far ones, a second round trip reads the rest of the channels.  No word is
-// read that lies further back than the blocks can hold tiles of the strip
-// (p.window), and where those are few the first round reads the tile before
-// alone: an older word has left L2 for memory, and a load from there, behind
-// the streams, took 2.7 us.  `meanwhile` runs under the first round.
+// its segment, word that of its words, tot the tile's maps of this lane's E
+// channels.  Publishes, waits, and returns the entering states.  Tiles whose
+// first row (in processing order) is a start enter with 0, which they never
+// use.  One round trip reads the words of the kNear tiles before for every
+// channel, and those of up to 32 more for the strip's first channel; if the
+// state is among the far ones, a second round trip reads the rest of the
+// channels.  No word is read that lies further back than the blocks can hold
+// tiles of the strip (p.window), and where those are few the first round
+// reads the tile before alone: an older word has left L2 for memory, and a
+// load from there, behind the streams, took 2.7 us.  `meanwhile` runs under
+// the first round.
 constexpr int kNear = 4;
 template <int E, class Meanwhile>
 __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int q, int word, bool last, int lane,
@@ -273,7 +262,7 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
     auto publish_state = [&] {
         if (last) return;
 #pragma unroll
-        for (int e = 0; e < E; ++e) st_relaxed_u32(p.carry + at + e, __float_as_uint(apply_map(tot[e].x, tot[e].y, hin[e])));
+        for (int e = 0; e < E; ++e) st_relaxed_u64(p.words + at + e, word_of(-0.f, apply_map(tot[e].x, tot[e].y, hin[e])));
     };
     if (fresh) {
         publish_state();
@@ -284,80 +273,53 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
         publish_state();
     } else if (!last) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) st_relaxed_u64(p.maps + at + e, pack_map(tot[e]));
+        for (int e = 0; e < E; ++e) st_relaxed_u64(p.words + at + e, word_of(tot[e].x, tot[e].y));
     }
     bool found = false;
     for (uint32_t polls = 0; !found; ++polls) {
         uint64_t m[kNear][E];
-        uint32_t st[kNear][E];
         const int reach = polls == 0 && p.window <= 8 ? 1 : (q < p.window ? q : p.window);
 #pragma unroll
         for (int i = 0; i < kNear; ++i) {
-            if (i < reach) {
-                load_states<E>(p.carry + at - (i + 1) * step, st[i]);
-                load_maps<E>(p.maps + at - (i + 1) * step, m[i]);
-            } else {
-                st[i][0] = kNone;
-                m[i][0] = ~uint64_t(0);
-            }
+            m[i][0] = kNone;
+            if (i < reach) load_words<E>(p.words + at - (i + 1) * step, m[i]);
         }
         const int far = 1 + kNear + lane;                          // this lane probes the tile that far before
-        uint32_t ps = kNone;
-        uint64_t pm = ~uint64_t(0);
-        if (far <= reach) {
-            ps = ld_relaxed_u32(p.carry + (word - far) * step + strip * TC);
-            pm = ld_relaxed_u64(p.maps + (word - far) * step + strip * TC);
-        }
+        uint64_t probe = kNone;
+        if (far <= reach) probe = ld_relaxed_u64(p.words + (word - far) * step + strip * TC);
         if (polls == 0) meanwhile();
-        int k = -1;                                                // nearest published state, maps there before it
+        int k = -1;                                                // nearest state, maps there before it
         bool there = true;
 #pragma unroll
         for (int i = 0; i < kNear; ++i) {
-            if (there && k < 0 && words_in<E>(st[i])) k = i;
             there = there && words_in<E>(m[i]);
+            if (there && k < 0 && words_cut<E>(m[i])) k = i;
         }
         if (__all_sync(0xffffffffu, k >= 0)) {
 #pragma unroll
-            for (int i = kNear - 1; i >= 0; --i) {
-                if (i == k) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) hin[e] = __uint_as_float(st[i][e]);
-                } else if (i < k) {
-                    apply_words<E>(m[i], hin);
-                }
-            }
+            for (int i = kNear - 1; i >= 0; --i)
+                if (i <= k) apply_words<E>(m[i], hin);
             found = true;
         } else if (__all_sync(0xffffffffu, there)) {
-            const uint32_t has_state = __ballot_sync(0xffffffffu, ps != kNone);
-            const uint32_t has_map = __ballot_sync(0xffffffffu, pm != ~uint64_t(0));
-            const int j = has_state ? __ffs(has_state) - 1 : 0;
+            const uint32_t in = __ballot_sync(0xffffffffu, probe != kNone);
+            const uint32_t state = __ballot_sync(0xffffffffu, probe != kNone && is_cut(word_a(probe)));
+            const int j = state ? __ffs(state) - 1 : 0;
             const uint32_t nearer = (1u << j) - 1u;
-            if (has_state && (has_map & nearer) == nearer) {
-                uint32_t s0[E];
-                load_states<E>(p.carry + at - (kNear + j + 1) * step, s0);
+            if (state && (in & nearer) == nearer) {
                 bool ok = true;
-                for (int i0 = j; i0 > 0; i0 -= 4) {                // maps of the far tiles, oldest first
+                for (int i0 = j; i0 >= 0; i0 -= 4) {               // the state, then the maps of the far tiles, oldest first
                     uint64_t w[4][E];
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        if (i0 - u > 0) load_maps<E>(p.maps + at - (kNear + i0 - u) * step, w[u]);
-                    if (i0 == j) {
-                        ok = words_in<E>(s0);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) hin[e] = __uint_as_float(s0[e]);
-                    }
+                        if (i0 - u >= 0) load_words<E>(p.words + at - (kNear + i0 - u + 1) * step, w[u]);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        if (i0 - u > 0) {
+                        if (i0 - u >= 0) {
                             ok = ok && words_in<E>(w[u]);
+                            if (i0 - u == j) ok = ok && words_cut<E>(w[u]);
                             apply_words<E>(w[u], hin);
                         }
                     }
-                }
-                if (j == 0) {
-                    ok = words_in<E>(s0);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) hin[e] = __uint_as_float(s0[e]);
                 }
 #pragma unroll
                 for (int i = kNear - 1; i >= 0; --i) apply_words<E>(m[i], hin);
@@ -970,36 +932,50 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             const auto dh = reader<IO, E, TMA, R, Shape, 2>(p, smem, n % S, warp, lane, row, d0, p.dh, p.dh_rs);
             const uint4 k = info.masks[warp];
             V A = vset<V>(1.f), B = vset<V>(0.f), RA = vset<V>(1.f), RB = vset<V>(0.f);
-            // a tile inside one sequence takes the rows without a branch, so that their
-            // loads and gates run side by side (with one a row: 148 us for this pass
-            // on bf16 16384 x 2048)
-            auto rows = [&](auto plain) {
-                constexpr bool PLAIN = decltype(plain)::value;
+            // rows without a branch, so that their loads and gates run side by side (with a
+            // branch for starts and ends in each: 148 us for this pass on bf16 16384 x 2048)
+            {
                 V a[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     V z;
                     s[r] = bwd_gate<GATE, IO>(f(r));
                     bwd_split<GATE>(s[r], a[r], z);
-                    if (!PLAIN && (k.x >> r & 1u)) {
-                        A = vset<V>(-0.f);
-                        B = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
-                    }
                     B = vfma(a[r], B, GATE == GATE_SIGMOID ? vmul(z, v(r)) : v(r));
                     A = vmul(A, a[r]);
                 }
 #pragma unroll
                 for (int r = R - 1; r >= 0; --r) {
-                    if (!PLAIN && (k.y >> r & 1u)) {
-                        RA = vset<V>(-0.f);
-                        RB = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
-                    }
                     RB = vmul(a[r], vadd(RB, dh(r)));
                     RA = vmul(RA, a[r]);
                 }
-            };
-            if (k.w) rows(std::true_type{});
-            else rows(std::false_type{});
+            }
+            if (!k.w) {                                               // few tiles: the folds again, row by row
+                A = RA = vset<V>(1.f);
+                B = RB = vset<V>(0.f);
+#pragma unroll 1
+                for (int r = 0; r < R; ++r) {
+                    V a, z;
+                    bwd_split<GATE>(bwd_gate<GATE, IO>(f(r)), a, z);
+                    if (k.x >> r & 1u) {
+                        A = vset<V>(-0.f);
+                        B = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
+                    }
+                    B = vfma(a, B, GATE == GATE_SIGMOID ? vmul(z, v(r)) : v(r));
+                    A = vmul(A, a);
+                }
+#pragma unroll 1
+                for (int r = R - 1; r >= 0; --r) {
+                    V a, z;
+                    bwd_split<GATE>(bwd_gate<GATE, IO>(f(r)), a, z);
+                    if (k.y >> r & 1u) {
+                        RA = vset<V>(-0.f);
+                        RB = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
+                    }
+                    RB = vmul(a, vadd(RB, dh(r)));
+                    RA = vmul(RA, a);
+                }
+            }
             if (!got) A = B = RA = RB = vset<V>(nan_value());
             blk.A[0][n % kQ][warp][lane] = RA;
             blk.B[0][n % kQ][warp][lane] = RB;
