@@ -877,10 +877,13 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
 // D per kBwdTR rows), instead of being read back: the outputs h are not
 // needed, so the pass reads three arrays and not four, and the states have
 // not been rounded to 16 bits.
+//
+// What a thread keeps of a gate: GATE_SIGMOID as forward; GATE_LOG: a, negated
+// where f > 0, which has no gradient.  (16-bit I/O with signed_small spent 13
+// of 52 instructions per element on telling the probabilities apart.)
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ V bwd_gate(V f) {
-    // GATE_SIGMOID: signed small probability; GATE_LOG: a, negated where f > 0, which has no gradient
-    if constexpr (GATE == GATE_SIGMOID) return vmap(f, [](float x) { return signed_small(x); });
+    if constexpr (GATE == GATE_SIGMOID) return fwd_gate<GATE, IO>(f);
     else
         return vmap(f, [](float x) {
             const float t = log_decay<sizeof(IO) == 4>(x);
@@ -888,10 +891,13 @@ __device__ __forceinline__ V bwd_gate(V f) {
         });
 }
 // (a, z) of it; z is 1 for GATE_LOG
-template <int GATE, class V>
+template <int GATE, typename IO, class V>
 __device__ __forceinline__ void bwd_split(V s, V &a, V &z) {
-    if constexpr (GATE == GATE_SIGMOID) {
+    if constexpr (GATE == GATE_SIGMOID && sizeof(IO) == 4) {
         split_small(s, a, z);
+    } else if constexpr (GATE == GATE_SIGMOID) {
+        a = s;
+        z = vfma(s, vset<V>(-1.f), vset<V>(1.f));
     } else {
         a = vmap(s, [](float x) { return fabsf(x); });
         z = vset<V>(1.f);
@@ -940,7 +946,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                 for (int r = 0; r < R; ++r) {
                     V z;
                     s[r] = bwd_gate<GATE, IO>(f(r));
-                    bwd_split<GATE>(s[r], a[r], z);
+                    bwd_split<GATE, IO>(s[r], a[r], z);
                     B = vfma(a[r], B, GATE == GATE_SIGMOID ? vmul(z, v(r)) : v(r));
                     A = vmul(A, a[r]);
                 }
@@ -956,7 +962,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
 #pragma unroll 1
                 for (int r = 0; r < R; ++r) {
                     V a, z;
-                    bwd_split<GATE>(bwd_gate<GATE, IO>(f(r)), a, z);
+                    bwd_split<GATE, IO>(bwd_gate<GATE, IO>(f(r)), a, z);
                     if (k.x >> r & 1u) {
                         A = vset<V>(-0.f);
                         B = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
@@ -967,7 +973,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
 #pragma unroll 1
                 for (int r = R - 1; r >= 0; --r) {
                     V a, z;
-                    bwd_split<GATE>(bwd_gate<GATE, IO>(f(r)), a, z);
+                    bwd_split<GATE, IO>(bwd_gate<GATE, IO>(f(r)), a, z);
                     if (k.y >> r & 1u) {
                         RA = vset<V>(-0.f);
                         RB = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
@@ -1002,7 +1008,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                     if (!PLAIN && (k.x >> r & 1u)) h = state_row<E>(p.h0, info.start[warp * R + r] * p.h0_ss, d0, p.D);
                     const V x = v(r);
                     V a, z;
-                    bwd_split<GATE>(s[r], a, z);
+                    bwd_split<GATE, IO>(s[r], a, z);
                     if constexpr (GATE == GATE_SIGMOID) {
                         c[r] = vmul(vmul(a, z), vfma(x, vset<V>(-1.f), h));
                         h = vfma(a, h, vmul(z, x));
@@ -1023,7 +1029,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                 for (int r = R - 1; r >= 0; --r) {
                     const V g = vadd(flow, dh(r));
                     V a, z;
-                    bwd_split<GATE>(s[r], a, z);
+                    bwd_split<GATE, IO>(s[r], a, z);
                     if (dvalid) {
                         __stcs(reinterpret_cast<W *>(pf), C::out(vmul(c[r], g)));
                         __stcs(reinterpret_cast<W *>(pv), C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g));
@@ -1038,7 +1044,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                     if (k.y >> r & 1u) flow = state_row<E>(p.dh_last, info.end[warp * R + r] * p.D, d0, p.D);
                     const V g = vadd(flow, dh(r));
                     V a, z;
-                    bwd_split<GATE>(s[r], a, z);
+                    bwd_split<GATE, IO>(s[r], a, z);
                     if (dvalid && row + r < info.row_end) {
                         const bool live = k.z >> r & 1u;
                         __stcs(reinterpret_cast<W *>(pf), live ? C::out(vmul(c[r], g)) : W(0));

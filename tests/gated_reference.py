@@ -13,7 +13,8 @@ rounding is |f| 2^-24 in the exponent):
   16-bit I/O, log: 2^-21 + |f| 2^-23 everywhere.
   16-bit I/O, sigmoid: a = 1 / (1 + 2^x), the sum rounded (2^-24) and the
            reciprocal off by 2^-23, so 2^-22 a on top of the above, and 1 - a
-           is off by as much and its own rounding, 2^-24.
+           is off by as much and its own rounding, 2^-24; the same in the
+           gradients.
 The hardware's 2^x gives 0 for results below 2^-126, the smallest normal
 number, so a probability or decay is off by at most 2^-126 there whatever its
 relative error: that much is added to each.
@@ -85,10 +86,11 @@ def grad64(f, v, h0, cu, gate, dh, dh_last, dtype=torch.float32):
             ge = re + eps * gm
             prev, pm, pe = (h[t - 1], hm[t - 1], hb[t - 1]) if t > lo else (h0[s], np.abs(h0[s]), 0.0)
             if gate == "sigmoid":
-                rel = (2.0 ** -20 + np.abs(f[t]) * 2.0 ** -22)
+                # fp32: 1 - a to its own relative precision; 16-bit: to that of a, and a rounding
+                ez = (2.0 ** -20 + np.abs(f[t]) * 2.0 ** -22) * z[t] if precise else ea[t] + 2.0 ** -24
                 c, cm = a[t] * z[t] * (prev - v[t]), a[t] * z[t] * (pm + np.abs(v[t]))
-                ce = a[t] * z[t] * pe + (rel + 4 * eps) * cm
-                dv[t], bv[t] = z[t] * g, z[t] * ge + (rel + 2 * eps) * z[t] * gm
+                ce = a[t] * z[t] * pe + (a[t] * ez + ea[t] * z[t]) * (pm + np.abs(v[t])) + 4 * eps * cm
+                dv[t], bv[t] = z[t] * g, z[t] * ge + ez * gm + 2 * eps * z[t] * gm
             else:
                 keep = np.where(f[t] <= 0, 1.0, 0.0)
                 c, cm = keep * a[t] * prev, keep * a[t] * pm
