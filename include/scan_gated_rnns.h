@@ -615,7 +615,7 @@ SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
  *                shared with another call that can run at the same time, nor
  *                with the entry points that keep hand-off words in theirs.
  * States and arithmetic are fp32.  A NaN or infinity stays within its sequence
- * and channel.  The result does not depend on how blocks are timed: equal
+ * and channel (behind an infinite state the sequence holds infinities or NaN).  The result does not depend on how blocks are timed: equal
  * calls give equal bits.  Calls may be captured.  A chunk that waited too long
  * leaves NaN and sets the workspace's first word to SGR_ERR_TIMEOUT (~0
  * otherwise, behind a call that needs a workspace).
@@ -670,7 +670,7 @@ SGR_API sgr_status_t gated_step(const void *f, int64_t f_row_stride, const void 
 
 /*
  * int8_quantize -- rows of x (rows, K) as whole numbers and one scale each:
- * scale = max |x| / 127 (at least 2^-100), q = x / scale to the nearest whole
+ * scale = max |x| times the fp32 1/127 (at least 2^-100), q = x / scale to the nearest whole
  * number (ties to even), decided on the exact quotient.  A row with an infinity
  * or NaN gets the scale NaN and q = 0.  Serves tokens and weights' channels.
  */

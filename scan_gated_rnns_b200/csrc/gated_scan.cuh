@@ -22,14 +22,13 @@
 // results do not depend on timing.  To have the state there when it is asked
 // for, the rows are cut at sequence starts into segments of about equal length
 // and the segments are worked on side by side, so that a tile's predecessor is
-// a round of blocks older (one segment: 64 strips of bf16 32768 x 4096 in 23
-// sequences waited 2.6 us a tile, half of that for the predecessor's own
-// fold).  A map, and then in its place the
-// state, is one 64-bit word per channel, ~0 before the launch and valid once
-// it is not (arithmetic never gives that NaN), so a look-back is one round
-// trip to L2, without flags or fences.  Blocks take tiles by ticket in the
-// order they run, so a wait is always for a tile that a running block holds;
-// waits are bounded.
+// a round of blocks older (with one segment the 64 strips of bf16 32768 x 4096
+// in 23 sequences waited 2.6 us a tile, half of that for the predecessor's own
+// fold).  A map, and then in its place the state, is one 64-bit word per
+// channel, ~0 before the launch and valid once it is not (arithmetic never
+// gives that NaN), so a look-back is one round trip to L2, without flags or
+// fences.  Blocks take tiles by ticket in the order they run, so a wait is
+// always for a tile that a running block holds; waits are bounded.
 //
 // One persistent block per SM.  The feeding warp keeps a ring of tiles in
 // shared memory filled by the tensor memory accelerator (TMA; rows that start
@@ -42,6 +41,14 @@
 // in each of two blocks per SM, which spent half its time waiting, 307 us on
 // bf16 32768 x 4096; evaluating the gates twice was bound by instruction
 // issue, 50 per element, 311 us.)
+//
+// Measured (B200, SM clock 1965 MHz; bytes = f, v in and h out, or f, v, dh in
+// and df, dv out, over the 6549 GB/s of a copy): forward fp32 131072 x 512
+// 157 us (0.78), fp32 8 x 4096 x 1024 81 us (0.76), bf16 32768 x 4096 in 23
+// sequences 169 us (0.73); backward fp32 8 x 4096 x 1024 127 us (0.81), bf16
+// 16384 x 2048 88 us (0.58).  Bound by: the wait for the carried state where
+// one long sequence keeps the segments at one; memory's latency behind its
+// own streams otherwise; instruction issue (49 % busy) in the 16-bit gradient.
 #pragma once
 
 #include "gated_math.cuh"

@@ -137,6 +137,7 @@ sgr_status_t product(const ProjectParams &p, sgr_dtype_t out, cudaStream_t s) {
                                                 : launch_tensor<__half>(p, sms, s);
         return e == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
     }
+    if ((p.M + 63) / 64 > 65535) return SGR_ERR_UNSUPPORTED;      // grid rows
     const dim3 grid(unsigned((p.N + 63) / 64), unsigned((p.M + 63) / 64));
     if (out == SGR_F32) int8_project_any_kernel<float><<<grid, 256, 0, s>>>(p);
     else if (out == SGR_BF16) int8_project_any_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
@@ -183,7 +184,6 @@ sgr_status_t int8_projection(const void *x, int64_t x_row_stride, sgr_dtype_t x_
     if (K == 0 || !x || !w || !w_scale || !y || (x_dtype == SGR_I8) != (x_scale != nullptr)) return SGR_ERR_INVALID_ARG;
     if (rows > 1 && y_row_stride < N) return SGR_ERR_INVALID_ARG;
     if (K > kMaxK || rows > kMaxDim || N > kMaxDim) return SGR_ERR_UNSUPPORTED;
-    if ((rows + 63) / 64 > 65535) return SGR_ERR_UNSUPPORTED;
     int64_t b_x, b_w, b_y, b_q;
     if (!host::span_ok(rows, K, x_row_stride, xsz, &b_x) || !host::span_ok(N, K, w_row_stride, 1, &b_w) ||
         !host::span_ok(rows, N, y_row_stride, ysz, &b_y) || !host::mul_ok(rows, pad16(K) + 4, &b_q))

@@ -32,8 +32,8 @@ __device__ __forceinline__ void put(const ProjectParams &p, int64_t m, int64_t n
 
 // ---------------------------------------------------------- quantisation
 //
-// s = max |x| / 127 (at least 2^-100), q = x / s to the nearest whole number,
-// ties to even.  The quotient is decided exactly: with q0 = rint(x (1 / s)),
+// s = max |x| times 1/127, both in fp32 (at least 2^-100), q = x / s to the
+// nearest whole number, ties to even.  The quotient is decided exactly: with q0 = rint(x (1 / s)),
 // off by one at most, the signs of the fused x - (q0 +- 1/2) s, which fma
 // rounds but never changes, say on which side of the half the quotient lies.
 // A row that holds an infinity or NaN gets the scale NaN and zeros, so its
@@ -87,15 +87,11 @@ struct QuantParams {
     int64_t rows, K;
 };
 
-// (scale, 1 / scale) of a row whose largest |x| is m.  m / 127 is rounded
-// correctly by one step from the product with the rounded reciprocal
-// (Markstein, 1990): the remainder m - 127 q is exact in an fma.  The second
-// value, the hardware's reciprocal, is 0 for a row that is not finite.
+// (scale, the hardware's 1 / scale) of a row whose largest |x| is m; the second
+// is 0 for a row that is not finite.
 __device__ __forceinline__ float2 row_scale(float m) {
     if (!(m <= 3.402823466e38f)) return make_float2(__int_as_float(0x7fffffff), 0.f);
-    constexpr float r = 1.f / 127.f;
-    const float q = m * r;
-    const float s = fmaxf(fmaf(fmaf(-127.f, q, m), r, q), kScaleFloor);
+    const float s = fmaxf(m * (1.f / 127.f), kScaleFloor);
     return make_float2(s, fast_rcp(s));
 }
 

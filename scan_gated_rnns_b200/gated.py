@@ -224,7 +224,9 @@ class GatedScan(torch.autograd.Function):
 def gated_scan_fn(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = None,
                   cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid"):
     """(h, h_last) of gated_scan with gradients for f, v and h0, from either
-    result."""
+    result (first derivatives only).  In a CUDA graph capture forward and
+    backward together, on leaves that no graph built outside the capture still
+    holds: PyTorch cannot capture a backward pass that reaches back to one."""
     return GatedScan.apply(f, v, h0, cu_seqlens, gate)
 
 

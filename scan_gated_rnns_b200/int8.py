@@ -18,8 +18,8 @@ from .gated import _DT, _dtype_code, _launch, _row_stride
 
 def int8_quantize(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """(q, scale) of x (..., K), float32, bfloat16 or float16: q int8 (..., K)
-    and scale float32 (...), scale = largest |x| of the row / 127 (at least
-    2^-100) and q = x / scale to the nearest whole number, ties to even.  The
+    and scale float32 (...), scale = largest |x| of the row times the float32
+    1/127 (at least 2^-100) and q = x / scale to the nearest whole number, ties to even.  The
     rows of q start on 16-byte boundaries, as the tensor-core projection takes
     them, for tokens and for a weight matrix's channels alike."""
     fn = "int8_quantize"

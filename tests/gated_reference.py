@@ -123,7 +123,7 @@ def quantize64(x):
     """q, scale (fp32) of float64 rows holding values of a narrower type."""
     with np.errstate(all="ignore"):
         m = np.abs(x).max(axis=1, initial=0.0).astype(np.float32)
-        s = np.maximum(m / np.float32(127.0), np.float32(2.0 ** -100))
+        s = np.maximum(m * (np.float32(1.0) / np.float32(127.0)), np.float32(2.0 ** -100))
         ok = np.isfinite(np.abs(x).sum(axis=1)) | np.isfinite(np.abs(x).max(axis=1, initial=0.0))
         q = np.where(ok[:, None], np.rint(x / s.astype(np.float64)[:, None]), 0)
     return q.astype(np.int64), np.where(ok, s, np.float32("nan"))

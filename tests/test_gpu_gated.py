@@ -457,3 +457,48 @@ def test_rows_cut_into_segments(bounds, dtype):
     odd.copy_(dh)
     for a, b in zip(sgr.gated_scan_backward(f, v, h0_d, states, odd, None, cu), (df, dv, d0)):
         assert torch.equal(a, b) or torch.allclose(a.float(), b.float(), rtol=0.02, atol=1e-4)
+
+
+def test_offsets_past_32_bits():
+    """Arrays of more than 2^31 elements: the last channels and rows against
+    the same columns in a call of their own (one sequence, so the rows are cut
+    into the same tiles and the bits are equal)."""
+    rows, D = 70016, 31360                                   # 2.2e9 elements, 4.4 GB each in bf16
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    f = torch.empty(rows, D, dtype=BF16, device=DEV).normal_(generator=g)
+    v = torch.empty(rows, D, dtype=BF16, device=DEV).normal_(generator=g)
+    h, last, states = sgr.gated_scan(f, v, save_states=True)
+    cols = slice(D - 64, D)
+    h1, last1, states1 = sgr.gated_scan(f[:, cols].contiguous(), v[:, cols].contiguous(), save_states=True)
+    assert torch.equal(h[:, cols], h1) and torch.equal(last[:, cols], last1)
+    df, dv, _ = sgr.gated_scan_backward(f, v, None, states, h)
+    df1, dv1, _ = sgr.gated_scan_backward(f[:, cols].contiguous(), v[:, cols].contiguous(), None, states1, h1)
+    assert torch.equal(df[:, cols], df1) and torch.equal(dv[:, cols], dv1)
+
+
+def test_autograd_captured_forward_and_backward():
+    torch.manual_seed(7)
+    shape = (2, 500, 64)
+    f, v, dh = (torch.randn(shape, device=DEV) for _ in range(3))
+    f.requires_grad_(True)
+    v.requires_grad_(True)
+
+    def step():
+        h, _ = sgr.gated_scan_fn(f, v)
+        return torch.autograd.grad(h, [f, v], dh)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            want = step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

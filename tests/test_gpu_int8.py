@@ -40,7 +40,7 @@ def test_quantize_ties_zeros_and_odd_rows():
     ties = torch.arange(-126, 127, dtype=F32) + 0.5
     x = torch.cat([ties, torch.tensor([127.0])])
     # and next to a half, one step of the type to either side, with a scale that is no power of two
-    s = np.float32(np.float32(5.3) / np.float32(127))
+    s = np.float32(np.float32(5.3) * (np.float32(1) / np.float32(127)))
     near = torch.from_numpy((np.arange(-126, 127) + 0.5).astype(np.float32) * s)
     rows = torch.stack([x, torch.cat([near, torch.tensor([5.3])]),
                         torch.cat([torch.nextafter(near, torch.tensor(1e9)), torch.tensor([5.3])]),
@@ -59,7 +59,7 @@ def test_quantize_ties_zeros_and_odd_rows():
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_scales_of_many_magnitudes(dtype):
-    """|x| / 127 rounded correctly, over all exponents; q is then 127 or -127."""
+    """|x| times 1/127 over all exponents; q is then 127 or -127."""
     rng = np.random.default_rng(5)
     x = rng.normal(size=300000) * np.exp2(rng.integers(-120, 120, 300000).astype(np.float64) * (0.1 if dtype == F16 else 1))
     x = torch.from_numpy(x).to(dtype)[:, None]
