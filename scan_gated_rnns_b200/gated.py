@@ -12,7 +12,7 @@ only; every operation runs in ``libsgr.so``):
 from __future__ import annotations
 
 import functools
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -127,6 +127,59 @@ def _scratch(need: int, device) -> Optional[torch.Tensor]:
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
+class _Call(NamedTuple):
+    """What a scan's arguments come to, beside their pointers."""
+    gate: int
+    dtype: int
+    f_rs: int
+    v_rs: int
+    rows: int
+    D: int
+    n: int
+    cu_bytes: int
+    need: int        # bytes of workspace
+    chunks: int      # rows of kept states
+
+
+def _call(fn: str, f: torch.Tensor, v: torch.Tensor, cu: Optional[torch.Tensor], gate: str) -> _Call:
+    g = _gate(gate)
+    f_rs = _operand(f, None, fn + ": f")
+    v_rs = _operand(v, f, fn + ": v")
+    dt = _dtype_code(f, fn)
+    rows, D, n, _, cb = _sequences(fn, f, cu)
+    return _Call(g, dt, f_rs, v_rs, rows, D, n, cb, *_sizes(rows, D))
+
+
+def _like(f: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(f) if f.is_contiguous() else torch.empty(f.shape, dtype=f.dtype, device=f.device)
+
+
+def _forward(c: _Call, f, v, hp, hss, cu, out, o_rs, zero, save_states):
+    device = f.device
+    h_last = torch.empty((c.n, c.D), dtype=torch.float32, device=device)
+    states = torch.empty((c.chunks, c.D), dtype=torch.float32, device=device) if save_states else None
+    ws = _scratch(c.need, device)
+    code = _launch(lib().gated_scan, device.index, f.data_ptr(), c.f_rs, v.data_ptr(), c.v_rs, hp, hss,
+                   cu.data_ptr() if c.cu_bytes else 0, c.cu_bytes, c.n, out.data_ptr(), o_rs, h_last.data_ptr(),
+                   states.data_ptr() if save_states else 0, c.rows, c.D, c.gate, c.dtype, zero,
+                   ws.data_ptr() if c.need else 0, c.need)
+    check("gated_scan", code)
+    return h_last, states
+
+
+def _backward(c: _Call, f, v, hp, hss, cu, states, dh, dh_rs, lp, want_dh0):
+    device = f.device
+    df, dv = _like(f), _like(f)
+    dh0 = torch.empty((c.n, c.D), dtype=torch.float32, device=device) if want_dh0 else None
+    ws = _scratch(c.need, device)
+    code = _launch(lib().gated_scan_backward, device.index, f.data_ptr(), c.f_rs, v.data_ptr(), c.v_rs, hp, hss,
+                   cu.data_ptr() if c.cu_bytes else 0, c.cu_bytes, c.n, states.data_ptr(), dh.data_ptr(), dh_rs, lp,
+                   df.data_ptr(), c.D, dv.data_ptr(), c.D, dh0.data_ptr() if want_dh0 else 0, c.rows, c.D, c.gate,
+                   c.dtype, ws.data_ptr() if c.need else 0, c.need)
+    check("gated_scan_backward", code)
+    return df, dv, dh0
+
+
 def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = None,
                cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid",
                out: Optional[torch.Tensor] = None, save_states: bool = False):
@@ -140,25 +193,14 @@ def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = No
     sequence.  h_last: float32 (S, D), the state behind each sequence.  With
     save_states a third result: what gated_scan_backward starts from."""
     fn = "gated_scan"
-    g = _gate(gate)
-    f_rs = _operand(f, None, fn + ": f")
-    v_rs = _operand(v, f, fn + ": v")
-    dt = _dtype_code(f, fn)
-    rows, D, n, cp, cb = _sequences(fn, f, cu_seqlens)
-    hp, hss = _states(h0, n, D, f, fn + ": h0", True)
-    zero = out is None
-    device = f.device
+    c = _call(fn, f, v, cu_seqlens, gate)
+    hp, hss = _states(h0, c.n, c.D, f, fn + ": h0", True)
+    zero, o_rs = out is None, c.D
     if zero:
-        out = torch.empty(f.shape, dtype=f.dtype, device=device)
-    o_rs = _operand(out, f, fn + ": out")
-    h_last = torch.empty((n, D), dtype=torch.float32, device=device)
-    need, chunks = _sizes(rows, D)
-    states = torch.empty((chunks, D), dtype=torch.float32, device=device) if save_states else None
-    ws = _scratch(need, device)
-    code = _launch(lib().gated_scan, device.index, f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n,
-                   out.data_ptr(), o_rs, h_last.data_ptr(), states.data_ptr() if save_states else 0, rows, D, g, dt,
-                   int(zero), ws.data_ptr() if need else 0, need)
-    check(fn, code)
+        out = _like(f)
+    else:
+        o_rs = _operand(out, f, fn + ": out")
+    h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, out, o_rs, int(zero), save_states)
     return (out, h_last, states) if save_states else (out, h_last)
 
 
@@ -169,41 +211,30 @@ def gated_scan_backward(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Ten
     h, h_last, states = gated_scan(f, v, h0, cu_seqlens, gate, save_states=True);
     dh0 is float32 (S, D), one row per sequence (None unless want_dh0)."""
     fn = "gated_scan_backward"
-    g = _gate(gate)
-    f_rs = _operand(f, None, fn + ": f")
-    v_rs = _operand(v, f, fn + ": v")
+    c = _call(fn, f, v, cu_seqlens, gate)
     dh_rs = _operand(dh, f, fn + ": dh")
-    dt = _dtype_code(f, fn)
-    rows, D, n, cp, cb = _sequences(fn, f, cu_seqlens)
-    hp, hss = _states(h0, n, D, f, fn + ": h0", True)
-    lp, lss = _states(dh_last, n, D, f, fn + ": dh_last", False)
-    if lp and n > 1 and lss != D:
+    hp, hss = _states(h0, c.n, c.D, f, fn + ": h0", True)
+    lp, lss = _states(dh_last, c.n, c.D, f, fn + ": dh_last", False)
+    if lp and c.n > 1 and lss != c.D:
         raise ValueError(f"{fn}: dh_last must be contiguous")
-    need, chunks = _sizes(rows, D)
-    sp, sss = _states(states, chunks, D, f, fn + ": states", False)
-    if states is None or (chunks > 1 and sss != D):
-        raise ValueError(f"{fn}: states must be the contiguous ({chunks}, {D}) tensor that gated_scan saved")
-    device = f.device
-    df = torch.empty(f.shape, dtype=f.dtype, device=device)
-    dv = torch.empty(f.shape, dtype=f.dtype, device=device)
-    dh0 = torch.empty((n, D), dtype=torch.float32, device=device) if want_dh0 else None
-    ws = _scratch(need, device)
-    code = _launch(lib().gated_scan_backward, device.index, f.data_ptr(), f_rs, v.data_ptr(), v_rs, hp, hss, cp, cb, n, sp,
-                   dh.data_ptr(), dh_rs, lp, df.data_ptr(), D, dv.data_ptr(), D, dh0.data_ptr() if want_dh0 else 0, rows,
-                   D, g, dt, ws.data_ptr() if need else 0, need)
-    check(fn, code)
-    return df, dv, dh0
+    _, sss = _states(states, c.chunks, c.D, f, fn + ": states", False)
+    if states is None or (c.chunks > 1 and sss != c.D):
+        raise ValueError(f"{fn}: states must be the contiguous ({c.chunks}, {c.D}) tensor that gated_scan saved")
+    return _backward(c, f, v, hp, hss, cu_seqlens, states, dh, dh_rs, lp, want_dh0)
 
 
 class GatedScan(torch.autograd.Function):
-    """The states that enter each chunk are kept for the backward pass (one
-    float32 row per 96 rows); the outputs are not."""
+    """The states inside the sequences are kept for the backward pass (about
+    one float32 row per 96 rows); the outputs are not."""
 
     @staticmethod
     def forward(ctx, f, v, h0, cu_seqlens, gate):
-        h, h_last, states = gated_scan(f, v, h0, cu_seqlens, gate, save_states=True)
+        c = _call("gated_scan", f, v, cu_seqlens, gate)
+        hp, hss = _states(h0, c.n, c.D, f, "gated_scan: h0", True)
+        h = _like(f)
+        h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, h, c.D, 1, True)
         ctx.save_for_backward(f, v, h0, cu_seqlens, states)
-        ctx.gate = gate
+        ctx.call = c
         ctx.set_materialize_grads(False)
         return h, h_last
 
@@ -213,9 +244,13 @@ class GatedScan(torch.autograd.Function):
         f, v, h0, cu_seqlens, states = ctx.saved_tensors
         if dh is None and dh_last is None:
             return None, None, None, None, None
-        dh = torch.zeros_like(f) if dh is None else dh.contiguous()
-        df, dv, dh0 = gated_scan_backward(f, v, h0, states, dh, None if dh_last is None else dh_last.contiguous(),
-                                          cu_seqlens, ctx.gate, want_dh0=h0 is not None and ctx.needs_input_grad[2])
+        # hooks on saved tensors may have laid them out anew
+        c = ctx.call._replace(f_rs=_row_stride(f, "f"), v_rs=_row_stride(v, "v"))
+        hp, hss = _states(h0, c.n, c.D, f, "h0", True)
+        dh = torch.zeros_like(f, memory_format=torch.contiguous_format) if dh is None else dh.contiguous()
+        last = None if dh_last is None else dh_last.contiguous()
+        df, dv, dh0 = _backward(c, f, v, hp, hss, cu_seqlens, states.contiguous(), dh, c.D,
+                                last.data_ptr() if last is not None else 0, ctx.needs_input_grad[2])
         if dh0 is not None and h0.dim() == 1:
             dh0 = dh0.sum(0)
         return df, dv, dh0, None, None

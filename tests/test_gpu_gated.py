@@ -502,3 +502,23 @@ def test_autograd_captured_forward_and_backward():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_saved_tensors_laid_out_anew():
+    """Hooks that move what is saved to the host and back give other strides."""
+    torch.manual_seed(9)
+    both = torch.randn(300, 96, device=DEV)
+    states = torch.randn(3, 96, device=DEV)
+    cu = torch.tensor([0, 10, 200, 300], device=DEV)
+    dh = torch.randn(300, 48, device=DEV)
+    got = []
+    for hooks in (False, True):
+        f, v = both[:, :48].detach().requires_grad_(True), both[:, 48:].detach().requires_grad_(True)
+        h0 = states[:, 5:53].detach().requires_grad_(True)
+        if hooks:
+            with torch.autograd.graph.save_on_cpu():
+                h, _ = sgr.gated_scan_fn(f, v, h0, cu)
+        else:
+            h, _ = sgr.gated_scan_fn(f, v, h0, cu)
+        got.append(torch.autograd.grad(h, [f, v, h0], dh))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
