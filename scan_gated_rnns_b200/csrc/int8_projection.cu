@@ -74,7 +74,7 @@ bool mappable(const int8_t *base, int64_t rows, int64_t rs) {
 }
 
 template <int NT, typename OUT>
-cudaError_t launch_split(const ProjectParams &p, int sms, cudaStream_t s) {
+cudaError_t launch_split(const ProjectParams &p, int sms, bool behind, cudaStream_t s) {
     using S = SplitShape<NT>;
     const int64_t ct = (p.N + 127) / 128, tt = (p.M + NT - 1) / NT, n_kb = (p.K + kKB - 1) / kKB;
     if (ct * tt > std::numeric_limits<int>::max() / 8) return cudaErrorInvalidConfiguration;
@@ -92,12 +92,14 @@ cudaError_t launch_split(const ProjectParams &p, int sms, cudaStream_t s) {
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = S::smem_bytes;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = unsigned(C);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = behind ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p, int(ct), C, map_w, map_x);
 }
 
@@ -116,25 +118,26 @@ cudaError_t launch_pair(const ProjectParams &p, int sms, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// `behind`: the quantising kernel of this call was the last launch on the stream.
 template <typename OUT>
-cudaError_t launch_tensor(const ProjectParams &p, int sms, cudaStream_t s) {
+cudaError_t launch_tensor(const ProjectParams &p, int sms, bool behind, cudaStream_t s) {
     const int64_t pairs = ((p.N + 255) / 256) * ((p.M + 255) / 256);
     if (p.M > 128 && 2 * pairs >= sms / 2) return launch_pair<OUT>(p, sms, s);
-    if (p.M <= 16) return launch_split<16, OUT>(p, sms, s);
-    if (p.M <= 32) return launch_split<32, OUT>(p, sms, s);
-    if (p.M <= 64) return launch_split<64, OUT>(p, sms, s);
-    return launch_split<128, OUT>(p, sms, s);
+    if (p.M <= 16) return launch_split<16, OUT>(p, sms, behind, s);
+    if (p.M <= 32) return launch_split<32, OUT>(p, sms, behind, s);
+    if (p.M <= 64) return launch_split<64, OUT>(p, sms, behind, s);
+    return launch_split<128, OUT>(p, sms, behind, s);
 }
 
-sgr_status_t product(const ProjectParams &p, sgr_dtype_t out, cudaStream_t s) {
+sgr_status_t product(const ProjectParams &p, sgr_dtype_t out, bool behind, cudaStream_t s) {
     if (mappable(p.w, p.N, p.w_rs) && mappable(p.x, p.M, p.x_rs)) {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return SGR_ERR_CUDA;
         const int sms = host::sm_count(dev);
         if (sms <= 1) return SGR_ERR_CUDA;
-        const cudaError_t e = out == SGR_F32    ? launch_tensor<float>(p, sms, s)
-                              : out == SGR_BF16 ? launch_tensor<__nv_bfloat16>(p, sms, s)
-                                                : launch_tensor<__half>(p, sms, s);
+        const cudaError_t e = out == SGR_F32    ? launch_tensor<float>(p, sms, behind, s)
+                              : out == SGR_BF16 ? launch_tensor<__nv_bfloat16>(p, sms, behind, s)
+                                                : launch_tensor<__half>(p, sms, behind, s);
         return e == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
     }
     if ((p.M + 63) / 64 > 65535) return SGR_ERR_UNSUPPORTED;      // grid rows
@@ -204,7 +207,7 @@ sgr_status_t int8_projection(const void *x, int64_t x_row_stride, sgr_dtype_t x_
         if (st != SGR_OK) return st;
         p.x = q; p.x_rs = pad16(K); p.x_scale = scale;
     }
-    return product(p, y_dtype, stream);
+    return product(p, y_dtype, x_dtype != SGR_I8, stream);
 }
 
 }  // extern "C"

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(256, NV >= 4 ? 4 : 6) int8_quantize_kernel(con
     int turn = 0;
     const int part = threadIdx.x % TPR;
     using W = typename Raw<IO, 1>::type;
+    asm volatile("griddepcontrol.launch_dependents;");     // a product behind it may set up now
     // a block reduction holds a barrier, so every thread of the block stays in the loop
     for (int64_t row0 = int64_t(blockIdx.x) * ROWS; row0 < p.rows; row0 += int64_t(gridDim.x) * ROWS) {
         const int64_t row = row0 + threadIdx.x / TPR;

@@ -75,6 +75,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// The kernel this one was launched behind as a dependent has ended and its
+// writes are there; returns at once where there is none.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 16 accumulator columns of this thread's lane; completes with tmem_wait
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -115,6 +119,11 @@ __device__ __forceinline__ void put4(const ProjectParams &p, int64_t m, int64_t 
 // memories and writes it.  The sums are whole numbers, so their order does
 // not matter.  With few tokens the weights' bytes are the work, and the split
 // is what spreads them over all SMs.
+//
+// Behind int8_quantize in one call the kernel is launched as its dependent
+// (programmatic launch): its blocks set up and start the copies of the weights
+// while the tokens are still being quantised, and wait for that kernel's end
+// before anything of x is touched.
 template <int NT>
 struct SplitShape {
     static constexpr uint32_t a_bytes = 128 * kKB, b_bytes = NT * kKB, stage_bytes = a_bytes + b_bytes;
@@ -163,9 +172,17 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
 
     if (warp == 0 && lane == 0) {
         int g = 0;
-        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        // the first stages' weights, before x may be there
+        for (; g < S::stages && kb0 + g < kb1; ++g) {
+            mbar_expect_tx(full(g), S::stage_bytes);
+            tma_load_2d(ring + uint32_t(g) * S::stage_bytes, &map_w, (kb0 + g) * kKB, ct * 128, full(g));
+        }
+        grid_dependency_wait();
+        for (int i = 0; i < g; ++i)
+            tma_load_2d(ring + uint32_t(i) * S::stage_bytes + S::a_bytes, &map_x, (kb0 + i) * kKB, tt * NT, full(i));
+        for (int kb = kb0 + g; kb < kb1; ++kb, ++g) {
             const int s = g % S::stages;
-            if (g >= S::stages && !mbar_wait(empty(s), uint32_t((g / S::stages - 1) & 1), kWait)) {
+            if (!mbar_wait(empty(s), uint32_t((g / S::stages - 1) & 1), kWait)) {
                 *s_bad = 1;
                 break;
             }
@@ -199,6 +216,7 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
     }
     __syncwarp();
     if (!mbar_wait(done, 0, kWait)) *s_bad = 1;
+    grid_dependency_wait();                                        // the tokens' scales
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;");
 
