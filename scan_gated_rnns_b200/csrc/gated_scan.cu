@@ -74,6 +74,22 @@ bool mappable(const void *base, int64_t rows, int64_t D, int64_t rs, int esz) {
     return host::aligned(base, 16) && (rows <= 1 || (rs * esz % 16 == 0 && rs >= D && rs * esz < (int64_t(1) << 40)));
 }
 
+// `behind`: as the dependent of the launch before, which cleared the workspace.
+template <class Kernel, class... Args>
+cudaError_t launch_behind(Kernel kernel, unsigned grid, size_t bytes, bool behind, cudaStream_t s, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename IO, int E, int GATE, bool TMA>
 cudaError_t launch(GatedParams p, bool backward, cudaStream_t s) {
     int dev = 0;
@@ -100,15 +116,15 @@ cudaError_t launch(GatedParams p, bool backward, cudaStream_t s) {
         auto kernel = gated_scan_backward_kernel<IO, E, GATE, TMA>;
         static_assert(bytes <= 227 * 1024, "one block per SM");
         if ((e = host::allow_smem<gated_scan_backward_kernel<IO, E, GATE, TMA>>(int(bytes))) != cudaSuccess) return e;
-        kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1], m[2]);
+        e = launch_behind(kernel, grid, bytes, p.ticket != nullptr, s, p, m[0], m[1], m[2]);
     } else {
         constexpr uint32_t bytes = ForwardShape<IO, E, TMA>::smem_bytes;
         auto kernel = gated_scan_kernel<IO, E, GATE, TMA>;
         static_assert(bytes <= 227 * 1024, "one block per SM");
         if ((e = host::allow_smem<gated_scan_kernel<IO, E, GATE, TMA>>(int(bytes))) != cudaSuccess) return e;
-        kernel<<<grid, kThreads, bytes, s>>>(p, m[0], m[1]);
+        e = launch_behind(kernel, grid, bytes, p.ticket != nullptr, s, p, m[0], m[1]);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename IO, int E, bool TMA>
@@ -195,7 +211,10 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
         p.ticket = reinterpret_cast<uint32_t *>(w + kTicketAt);
         p.words = reinterpret_cast<uint64_t *>(w + kHeader);
         // nothing of an earlier call is read
-        if (cudaMemsetAsync(w, 0xff, l.total, stream) != cudaSuccess) return SGR_ERR_CUDA;
+        const int64_t n = int64_t(l.total / 16);
+        gated_clear_kernel<<<unsigned(std::min<int64_t>((n + 255) / 256, 148 * 4)), 256, 0, stream>>>(
+            reinterpret_cast<uint4 *>(w), n);
+        if (cudaGetLastError() != cudaSuccess) return SGR_ERR_CUDA;
     }
     return launch_any(p, dtype, gate == SGR_GATE_LOG ? GATE_LOG : GATE_SIGMOID, E, backward, stream) == cudaSuccess
                ? SGR_OK

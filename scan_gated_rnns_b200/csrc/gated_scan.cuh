@@ -375,6 +375,17 @@ __device__ __forceinline__ void put_state_row(float *base, int64_t off, int64_t 
     }
 }
 
+// The scan is launched as the dependent of the kernel that sets its workspace
+// to ~0 (programmatic launch), so that its blocks are set up by the time the
+// words are: whoever touches the workspace waits here first.
+__device__ __forceinline__ void workspace_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__global__ void __launch_bounds__(256) gated_clear_kernel(uint4 *p, int64_t n) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256)
+        p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
 // ------------------------------------------------------ inside a block
 //
 // Tile n of the block lies in slot n % S from its copies until every data
@@ -522,13 +533,6 @@ template <int S, int OPS, int TR, uint32_t OP_BYTES, int TC, bool TMA, class B>
 __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slots, int lane, bool reverse,
                                      const CUtensorMap *m0, const CUtensorMap *m1, const CUtensorMap *m2) {
     Waiter wait{p.status, kTileWait};
-    // the next ticket is drawn a tile ahead, so that its round trip passes under the work on this one
-    uint32_t ticket = 0;
-    if (p.ticket) {
-        if (lane == 0) ticket = atomicAdd(p.ticket, 1u) + 1u;
-    } else {
-        ticket = blockIdx.x;
-    }
     const bool held = p.cu != nullptr && p.n_seqs < kBoundsHeld;
     if (held)
         for (int i = lane; i <= int(p.n_seqs); i += 32) blk.bounds[i] = cu_at(p, i);
@@ -536,6 +540,14 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
     __syncwarp();
     Segments<TR> seg;
     seg.init(p, bounds, lane);
+    // the next ticket is drawn a tile ahead, so that its round trip passes under the work on this one
+    uint32_t ticket = 0;
+    if (p.ticket) {
+        workspace_ready();
+        if (lane == 0) ticket = atomicAdd(p.ticket, 1u) + 1u;
+    } else {
+        ticket = blockIdx.x;
+    }
     uint64_t once;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     int ends = 0;
@@ -620,6 +632,7 @@ template <int E, int S, int TR, int DIR, class B>
 __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, int lane) {
     using V = typename FVec<E>::type;
     Waiter wait{p.status, kTileWait};
+    workspace_ready();
     for (int n = c;; n += kCarryWarps) {
         wait(&blk.full[n % S], n / S);
         const TileInfo<TR> &info = blk.info[n % S];
