@@ -44,11 +44,12 @@
 //
 // Measured (B200, SM clock 1965 MHz; bytes = f, v in and h out, or f, v, dh in
 // and df, dv out, over the 6549 GB/s of a copy): forward fp32 131072 x 512
-// 157 us (0.78), fp32 8 x 4096 x 1024 81 us (0.76), bf16 32768 x 4096 in 23
-// sequences 169 us (0.73); backward fp32 8 x 4096 x 1024 127 us (0.81), bf16
-// 16384 x 2048 88 us (0.58).  Bound by: the wait for the carried state where
-// one long sequence keeps the segments at one; memory's latency behind its
-// own streams otherwise; instruction issue (49 % busy) in the 16-bit gradient.
+// 154 us (0.80), fp32 8 x 4096 x 1024 79 us (0.78), bf16 32768 x 4096 in 23
+// sequences 165 us (0.74); backward fp32 8 x 4096 x 1024 125 us (0.82), bf16
+// 16384 x 2048 85 us (0.60).  Bound by: the wait for the carried state where
+// one long sequence keeps the segments at one; memory at about 5.6 TB/s and
+// some 10 us of start and end otherwise; instruction issue (49 % busy) in the
+// 16-bit gradient.
 #pragma once
 
 #include "gated_math.cuh"

@@ -123,7 +123,10 @@ __device__ __forceinline__ void put4(const ProjectParams &p, int64_t m, int64_t 
 // Behind int8_quantize in one call the kernel is launched as its dependent
 // (programmatic launch): its blocks set up and start the copies of the weights
 // while the tokens are still being quantised, and wait for that kernel's end
-// before anything of x is touched.
+// before anything of x is touched.  Measured: 8 x 1024 x 2048 8 us, 120 x 4096
+// x 8192 17 us (its 33.5 MB of weights take 5 us from memory), 1111 x 1000 x
+// 1502 to fp32 13.8 us; bound by the start of a block, its few stages and the
+// cluster's two barriers, one after the other.
 template <int NT>
 struct SplitShape {
     static constexpr uint32_t a_bytes = 128 * kKB, b_bytes = NT * kKB, stage_bytes = a_bytes + b_bytes;
@@ -319,7 +322,9 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
 // tokens.  Against a tile of 128 x 256 per SM this needs two thirds of the
 // bytes from L2 for the same product, which is what bounds an 8-bit product
 // of this size first.  Two accumulators: the epilogue of a tile runs under
-// the next one's product.
+// the next one's product.  Measured: 8192 x 4096 x 8192 to bf16 198 us, 2.8
+// POP/s, 0.85 of twice the bf16 rate of a large library product; the tensor
+// cores' rate under the power limit bounds it.
 namespace pair {
 constexpr int kStages = 6;
 constexpr uint32_t kHalf = 128 * kKB;                      // one operand's share per block and stage

@@ -150,10 +150,6 @@ def _call(fn: str, f: torch.Tensor, v: torch.Tensor, cu: Optional[torch.Tensor],
     return _Call(g, dt, f_rs, v_rs, rows, D, n, cb, *_sizes(rows, D))
 
 
-def _like(f: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(f) if f.is_contiguous() else torch.empty(f.shape, dtype=f.dtype, device=f.device)
-
-
 def _forward(c: _Call, f, v, hp, hss, cu, out, o_rs, zero, save_states):
     device = f.device
     h_last = torch.empty((c.n, c.D), dtype=torch.float32, device=device)
@@ -169,7 +165,7 @@ def _forward(c: _Call, f, v, hp, hss, cu, out, o_rs, zero, save_states):
 
 def _backward(c: _Call, f, v, hp, hss, cu, states, dh, dh_rs, lp, want_dh0):
     device = f.device
-    df, dv = _like(f), _like(f)
+    df, dv = torch.empty_like(f), torch.empty_like(f)
     dh0 = torch.empty((c.n, c.D), dtype=torch.float32, device=device) if want_dh0 else None
     ws = _scratch(c.need, device)
     code = _launch(lib().gated_scan_backward, device.index, f.data_ptr(), c.f_rs, v.data_ptr(), c.v_rs, hp, hss,
@@ -197,7 +193,7 @@ def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = No
     hp, hss = _states(h0, c.n, c.D, f, fn + ": h0", True)
     zero, o_rs = out is None, c.D
     if zero:
-        out = _like(f)
+        out = torch.empty_like(f)              # rows of any spacing: those of the result are dense
     else:
         o_rs = _operand(out, f, fn + ": out")
     h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, out, o_rs, int(zero), save_states)
@@ -231,7 +227,7 @@ class GatedScan(torch.autograd.Function):
     def forward(ctx, f, v, h0, cu_seqlens, gate):
         c = _call("gated_scan", f, v, cu_seqlens, gate)
         hp, hss = _states(h0, c.n, c.D, f, "gated_scan: h0", True)
-        h = _like(f)
+        h = torch.empty_like(f)
         h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, h, c.D, 1, True)
         ctx.save_for_backward(f, v, h0, cu_seqlens, states)
         ctx.call = c
@@ -276,31 +272,33 @@ def gated_step(f: torch.Tensor, v: torch.Tensor, state: torch.Tensor, slots: Opt
     tokens in row order."""
     fn = "gated_step"
     g = _gate(gate)
-    f_rs = _operand(f, None, fn + ": f")
+    f_rs = _operand(f, None, "gated_step: f")
     if f.dim() != 2:
         raise ValueError(f"{fn}: f must be (M, D), got shape {tuple(f.shape)}")
-    v_rs = _operand(v, f, fn + ": v")
+    v_rs = _operand(v, f, "gated_step: v")
     dt = _dtype_code(f, fn)
     M, D = f.shape
+    n_slots = state.shape[0] if state.dim() == 2 else 0
     if state.dim() != 2 or state.shape[1] != D:
         raise ValueError(f"{fn}: state must be (slots, {D}), got {tuple(state.shape)}")
-    sp, srs = _states(state, state.shape[0], D, f, fn + ": state", False)
+    sp, srs = _states(state, n_slots, D, f, "gated_step: state", False)
+    device = f.get_device()
     kp = kb = 0
     if slots is not None:
-        ops._need_cuda(slots, fn + ": slots")
+        ops._need_cuda(slots, "gated_step: slots")
         if slots.dtype not in _INDEX or slots.dim() != 1 or slots.shape[0] != M or not slots.is_contiguous() or \
-                slots.get_device() != f.get_device():
+                slots.get_device() != device:
             raise ValueError(f"{fn}: slots must be a contiguous ({M},) int32 or int64 vector on {f.device}")
         kp, kb = slots.data_ptr(), _INDEX[slots.dtype]
-    elif state.shape[0] < M:
-        raise ValueError(f"{fn}: state has {state.shape[0]} rows for {M} requests")
-    zero = out is None
+    elif n_slots < M:
+        raise ValueError(f"{fn}: state has {n_slots} rows for {M} requests")
+    zero, o_rs = out is None, D
     if zero:
-        out = torch.empty((M, D), dtype=f.dtype, device=f.device)
-        o_rs = D
+        out = torch.empty_like(f)
     else:
-        o_rs = _operand(out, f, fn + ": out")
-    code = _launch(lib().gated_step, f.get_device(), f.data_ptr(), f_rs, v.data_ptr(), v_rs, sp, srs, state.shape[0], kp, kb,
-                   out.data_ptr(), o_rs, M, D, g, dt, int(zero))
-    check(fn, code)
+        o_rs = _operand(out, f, "gated_step: out")
+    code = _launch(lib().gated_step, device, f.data_ptr(), f_rs, v.data_ptr(), v_rs, sp, srs, n_slots, kp, kb,
+                   out.data_ptr(), o_rs, M, D, g, dt, zero)
+    if code:
+        check(fn, code)
     return out

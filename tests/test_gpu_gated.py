@@ -522,3 +522,24 @@ def test_saved_tensors_laid_out_anew():
             h, _ = sgr.gated_scan_fn(f, v, h0, cu)
         got.append(torch.autograd.grad(h, [f, v, h0], dh))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_broadcast_operands_and_their_gradients():
+    """One row of values for every token (row stride 0): read in place, its
+    gradient the sum over the rows; a batch dimension of stride 0 is refused."""
+    torch.manual_seed(4)
+    T, D = 250, 40
+    f = torch.randn(T, D, device=DEV, requires_grad=True)
+    row = torch.randn(1, D, device=DEV, requires_grad=True)
+    dh = torch.randn(T, D, device=DEV)
+    h, _ = sgr.gated_scan_fn(f, row.expand(T, D))
+    got = torch.autograd.grad(h, [f, row], dh)
+    f64 = f.detach().double().cpu().numpy()
+    v64 = row.detach().double().cpu().numpy().repeat(T, 0)
+    want, _, b, _ = scan64(f64, v64, np.zeros((1, D)), [0, T], "sigmoid")
+    check(h, want, b, F32, "h")
+    wf, wv, _, bf, bv, _ = grad64(f64, v64, np.zeros((1, D)), [0, T], "sigmoid", dh.double().cpu().numpy(), None)
+    check(got[0], wf, bf, F32, "df")
+    check(got[1], wv.sum(0, keepdims=True), (bv + T * 2.0 ** -24 * np.abs(wv)).sum(0, keepdims=True), F32, "row")
+    with pytest.raises(ValueError, match="evenly spaced"):
+        sgr.gated_scan(f[None].expand(2, T, D), f[None].expand(2, T, D))
