@@ -59,16 +59,11 @@ bool sizes_ok(int64_t rows, int64_t D) {
 // Tensor map of (rows, D) for boxes of 128 bytes x tr rows; what lies past
 // the edges reads as zero.
 bool tile_map(CUtensorMap *map, const void *base, int64_t rows, int64_t D, int64_t rs, int esz, int tr) {
-    const host::EncodeTiledFn enc = host::encode_tiled();
-    if (!enc) return false;
     const cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {rows > 1 ? cuuint64_t(rs) * esz : align_up(size_t(D) * esz, 16)};
+    const cuuint64_t row_bytes = rows > 1 ? cuuint64_t(rs) * esz : align_up(size_t(D) * esz, 16);
     const cuuint32_t box[2] = {cuuint32_t(128 / esz), cuuint32_t(tr)};
-    const cuuint32_t es[2] = {1u, 1u};
-    return enc(map, esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
-               const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return host::encode_rows(map, esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, base,
+                             dims, row_bytes, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 bool mappable(const void *base, int64_t rows, int64_t D, int64_t rs, int esz) {
     return host::aligned(base, 16) && (rows <= 1 || (rs * esz % 16 == 0 && rs >= D && rs * esz < (int64_t(1) << 40)));

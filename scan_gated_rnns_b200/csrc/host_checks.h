@@ -82,6 +82,24 @@ inline EncodeTiledFn encode_tiled() {
     return f;
 }
 
+// A tensor map of (rows, elements of a row).  The driver's encoder wants the
+// device's context current on the calling thread, and a thread that has made
+// no launch yet (a backward pass on its own thread) may not have it so: then
+// the device is set, as launches do by themselves, and the map encoded again.
+inline bool encode_rows(CUtensorMap *map, CUtensorMapDataType type, const void *base, const cuuint64_t (&dims)[2],
+                        cuuint64_t row_bytes, const cuuint32_t (&box)[2], CUtensorMapSwizzle swizzle) {
+    const EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t es[2] = {1u, 1u};
+    const auto encode = [&] {
+        return enc(map, type, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    int dev = 0;
+    return encode() || (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode());
+}
+
 // Dynamic shared memory of a kernel, set once per kernel and device.
 template <auto KERNEL>
 inline cudaError_t allow_smem(int bytes) {

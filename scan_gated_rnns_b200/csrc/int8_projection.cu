@@ -57,15 +57,10 @@ sgr_status_t quantize(const QuantParams &p, sgr_dtype_t dtype, cudaStream_t s) {
 // Tensor map of 8-bit rows for boxes of 128 bytes x `box` rows, 128-byte
 // swizzle; bytes past the rows' ends read as zero.
 bool row_map(CUtensorMap *map, const int8_t *base, int64_t rows, int64_t K, int64_t rs, int box) {
-    const host::EncodeTiledFn enc = host::encode_tiled();
-    if (!enc) return false;
     const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(rows > 1 ? rs : pad16(K))};
     const cuuint32_t boxes[2] = {cuuint32_t(kKB), cuuint32_t(box)};
-    const cuuint32_t es[2] = {1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, boxes, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return host::encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, cuuint64_t(rows > 1 ? rs : pad16(K)),
+                             boxes, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Rows that a tensor map can describe.

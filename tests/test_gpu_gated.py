@@ -1,6 +1,8 @@
 """gated_scan, gated_scan_backward, gated_step and gated_scan_fn on the GPU
 against the recurrence in 64 bits, token by token (gated_reference.py holds
 the error bounds and their derivation)."""
+import concurrent.futures
+
 import numpy as np
 import pytest
 import torch
@@ -543,3 +545,24 @@ def test_broadcast_operands_and_their_gradients():
     check(got[1], wv.sum(0, keepdims=True), (bv + T * 2.0 ** -24 * np.abs(wv)).sum(0, keepdims=True), F32, "row")
     with pytest.raises(ValueError, match="evenly spaced"):
         sgr.gated_scan(f[None].expand(2, T, D), f[None].expand(2, T, D))
+
+
+def in_new_thread(work):
+    with concurrent.futures.ThreadPoolExecutor(1) as pool:
+        return pool.submit(work).result(timeout=60)
+
+
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16, torch.float16])
+def test_first_call_of_a_thread(dtype):
+    """A thread that has launched nothing yet, with memory at hand: short
+    scans (one tile, no workspace to clear first) in both directions."""
+    f = torch.randn(2, 24, 64, device=DEV).to(dtype)
+    v, dh = torch.randn_like(f), torch.randn_like(f)
+    *want, states = sgr.gated_scan(f, v, save_states=True)
+    back = sgr.gated_scan_backward(f, v, None, states, dh)
+    torch.cuda.synchronize()
+    got = in_new_thread(lambda: sgr.gated_scan(f, v))
+    grads = in_new_thread(lambda: sgr.gated_scan_backward(f, v, None, states, dh))
+    torch.cuda.synchronize()
+    for a, b in zip([*got, *grads], [*want, *back]):
+        assert (a is None and b is None) or torch.equal(a, b)

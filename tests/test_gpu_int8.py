@@ -4,6 +4,8 @@
 Tolerances: the sum is exact; float(sum) rounds once (2^-24), then one product
 and one fma round once each, so y is within 3 2^-24 (|s_x s_w sum| + |bias|)
 before the half step of its type."""
+import concurrent.futures
+
 import numpy as np
 import pytest
 import torch
@@ -231,3 +233,17 @@ def test_projection_scan_and_steps(gate):
         y64 = y.double().cpu().numpy()
         want, _, b, _ = scan64(y64[:, :D], y64[:, D:], before[[4, 0, 2]], [0, 1, 2, 3], gate, BF16)
         check(out, want, b, BF16, "token")
+
+
+@pytest.mark.parametrize("M", [4, 300])
+def test_first_call_of_a_thread(M):
+    """A thread that has launched nothing yet, with memory at hand."""
+    rng = np.random.default_rng(M)
+    x, w = (torch.from_numpy(whole(rng, rows, 256).astype(np.int8)).to(DEV) for rows in (M, 384))
+    sx, sw = torch.rand(M, device=DEV), torch.rand(384, device=DEV)
+    want = sgr.int8_projection(x, w, sw, x_scale=sx)
+    torch.cuda.synchronize()
+    with concurrent.futures.ThreadPoolExecutor(1) as pool:
+        got = pool.submit(lambda: sgr.int8_projection(x, w, sw, x_scale=sx)).result(timeout=60)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
