@@ -547,6 +547,28 @@ def test_broadcast_operands_and_their_gradients():
         sgr.gated_scan(f[None].expand(2, T, D), f[None].expand(2, T, D))
 
 
+def test_many_sequences_most_of_them_empty():
+    rng = np.random.default_rng(3)
+    rows, D, n = 900, 20, 30000
+    bounds = np.sort(rng.integers(0, rows + 1, n - 1)).tolist()
+    cu = [0, *bounds, rows]
+    f, v, f64, v64 = make(rng, "log", rows, D, F32)
+    h0 = rng.normal(size=(n, D)).astype(np.float32)
+    h0_d, cu_d = torch.from_numpy(h0).to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV)
+    h, last, states = sgr.gated_scan(f, v, h0_d, cu_d, "log", save_states=True)
+    want, wl, bh, bl = scan64(f64, v64, h0.astype(np.float64), cu, "log")
+    check(h, want, bh, F32, "h")
+    check(last, wl, bl, F32, "h_last")
+    dh = torch.randn(rows, D, device=DEV)
+    dl = torch.randn(n, D, device=DEV)
+    df, dv, d0 = sgr.gated_scan_backward(f, v, h0_d, states, dh, dl, cu_d, "log")
+    wf, wv, w0, bf, bv, b0 = grad64(f64, v64, h0.astype(np.float64), cu, "log", dh.double().cpu().numpy(),
+                                    dl.double().cpu().numpy())
+    check(df, wf, bf, F32, "df")
+    check(dv, wv, bv, F32, "dv")
+    check(d0, w0, b0, F32, "dh0")
+
+
 def in_new_thread(work):
     with concurrent.futures.ThreadPoolExecutor(1) as pool:
         return pool.submit(work).result(timeout=60)
