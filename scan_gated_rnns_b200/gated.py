@@ -39,6 +39,11 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name}: dtype {t.dtype} is not supported (float32, bfloat16 or float16)") from None
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """An empty result of t's shape with dense rows (t's own may overlap)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 # the raw handle of a device's current stream (a step is short beside the
 # objects that the public call builds)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -165,7 +170,7 @@ def _forward(c: _Call, f, v, hp, hss, cu, out, o_rs, zero, save_states):
 
 def _backward(c: _Call, f, v, hp, hss, cu, states, dh, dh_rs, lp, want_dh0):
     device = f.device
-    df, dv = torch.empty_like(f), torch.empty_like(f)
+    df, dv = _dense(f), _dense(f)
     dh0 = torch.empty((c.n, c.D), dtype=torch.float32, device=device) if want_dh0 else None
     ws = _scratch(c.need, device)
     code = _launch(lib().gated_scan_backward, device.index, f.data_ptr(), c.f_rs, v.data_ptr(), c.v_rs, hp, hss,
@@ -193,7 +198,7 @@ def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = No
     hp, hss = _states(h0, c.n, c.D, f, fn + ": h0", True)
     zero, o_rs = out is None, c.D
     if zero:
-        out = torch.empty_like(f)              # rows of any spacing: those of the result are dense
+        out = _dense(f)
     else:
         o_rs = _operand(out, f, fn + ": out")
     h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, out, o_rs, int(zero), save_states)
@@ -227,7 +232,7 @@ class GatedScan(torch.autograd.Function):
     def forward(ctx, f, v, h0, cu_seqlens, gate):
         c = _call("gated_scan", f, v, cu_seqlens, gate)
         hp, hss = _states(h0, c.n, c.D, f, "gated_scan: h0", True)
-        h = torch.empty_like(f)
+        h = _dense(f)
         h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, h, c.D, 1, True)
         ctx.save_for_backward(f, v, h0, cu_seqlens, states)
         ctx.call = c
@@ -294,7 +299,7 @@ def gated_step(f: torch.Tensor, v: torch.Tensor, state: torch.Tensor, slots: Opt
         raise ValueError(f"{fn}: state has {n_slots} rows for {M} requests")
     zero, o_rs = out is None, D
     if zero:
-        out = torch.empty_like(f)
+        out = _dense(f)
     else:
         o_rs = _operand(out, f, "gated_step: out")
     code = _launch(lib().gated_step, device, f.data_ptr(), f_rs, v.data_ptr(), v_rs, sp, srs, n_slots, kp, kb,
