@@ -748,19 +748,12 @@ __device__ __forceinline__ RowReader<IO, E, TMA, R> reader(const GatedParams &p,
 // ------------------------------------------------------------- forward
 //
 // What a thread keeps of an element between fold and replay, and the step.
-// 16-bit I/O: a = sigmoid(f) = 1 / (1 + 2^(-f log2 e)) to about 2^-22 and
-// z = 1 - a, which is where fp32 itself ends for a near 1; half a step of a
-// 16-bit f moves z by 2^-12 |f| of itself or more, as much as 2^-22 does at
-// f = 8.  fp32 I/O: signed_small, either probability to its own precision.
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ V fwd_gate(V f) {
     if constexpr (GATE == GATE_LOG) {
         return vmap(f, [](float x) { return log_decay<sizeof(IO) == 4>(x); });
-    } else if constexpr (sizeof(IO) == 4) {
-        return vmap(f, [](float x) { return signed_small(x); });
     } else {
-        const V e = vmap(vmul(f, vset<V>(kNegLog2e)), [](float x) { return fast_exp2(x); });
-        return vmap(vadd(e, vset<V>(1.f)), [](float x) { return fast_rcp(x); });
+        return hold_gate<IO>(f);
     }
 }
 template <int GATE, typename IO, class V>
@@ -768,13 +761,10 @@ __device__ __forceinline__ void fwd_step(V g, V v, V &a, V &b) {
     if constexpr (GATE == GATE_LOG) {
         a = g;
         b = v;
-    } else if constexpr (sizeof(IO) == 4) {
-        V z;
-        split_small(g, a, z);
-        b = vmul(z, v);
     } else {
-        a = g;
-        b = vmul(vfma(g, vset<V>(-1.f), vset<V>(1.f)), v);
+        V z;
+        open_gate<IO>(g, a, z);
+        b = vmul(z, v);
     }
 }
 
@@ -911,8 +901,7 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
 // not been rounded to 16 bits.
 //
 // What a thread keeps of a gate: GATE_SIGMOID as forward; GATE_LOG: a, negated
-// where f > 0, which has no gradient.  (16-bit I/O with signed_small spent 13
-// of 52 instructions per element on telling the probabilities apart.)
+// where f > 0, which has no gradient.
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ V bwd_gate(V f) {
     if constexpr (GATE == GATE_SIGMOID) return fwd_gate<GATE, IO>(f);
@@ -925,11 +914,8 @@ __device__ __forceinline__ V bwd_gate(V f) {
 // (a, z) of it; z is 1 for GATE_LOG
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ void bwd_split(V s, V &a, V &z) {
-    if constexpr (GATE == GATE_SIGMOID && sizeof(IO) == 4) {
-        split_small(s, a, z);
-    } else if constexpr (GATE == GATE_SIGMOID) {
-        a = s;
-        z = vfma(s, vset<V>(-1.f), vset<V>(1.f));
+    if constexpr (GATE == GATE_SIGMOID) {
+        open_gate<IO>(s, a, z);
     } else {
         a = vmap(s, [](float x) { return fabsf(x); });
         z = vset<V>(1.f);

@@ -38,3 +38,65 @@ def test_sliding_window(rows, D, dtype):
     y = sgr.gated_step(f, v, state)
     want, _, b, _ = scan64(f64, v64, np.zeros((rows, D)), list(range(rows + 1)), "sigmoid", dtype)
     check(y, want, b, dtype, "step")
+
+
+# --------------------------------------------------- gates far on one side
+#
+# 16-bit I/O has to keep both probabilities to their own precision as fp32 I/O
+# does (an fp32 state holds them, and bf16 holds dv = z g down to 2^-126), so
+# its bounds are those of the fp32 evaluation and the rounding of its type.
+def operands(dtype, f, seed, n=1):
+    rng = np.random.default_rng(seed)
+    rows, D = f.shape
+    f = torch.from_numpy(f).to(dtype)
+    v, dh = (torch.from_numpy(rng.normal(size=(rows, D))).to(dtype) for _ in range(2))
+    h0, dl = (torch.from_numpy(rng.normal(size=(n, D))).float() for _ in range(2))
+    return [x.to(DEV) for x in (f, v, dh, h0, dl)], [x.double().numpy() for x in (f, v, dh, h0, dl)]
+
+
+def both_directions(dtype, gate, f, cu, seed=0):
+    (f, v, dh, h0, dl), (f64, v64, dh64, h64, l64) = operands(dtype, f, seed, len(cu) - 1)
+    cu_d = torch.tensor(cu, device=DEV)
+    h, last, states = sgr.gated_scan(f, v, h0, cu_d, gate, save_states=True)
+    want, wl, bh, bl = scan64(f64, v64, h64, cu, gate)
+    check(h, want, bh, dtype, "h")
+    check(last, wl, bl, F32, "h_last")
+    df, dv, d0 = sgr.gated_scan_backward(f, v, h0, states, dh, dl, cu_d, gate)
+    wf, wv, w0, bf, bv, b0 = grad64(f64, v64, h64, cu, gate, dh64, l64)
+    check(df, wf, bf, dtype, "df")
+    check(dv, wv, bv, dtype, "dv")
+    check(d0, w0, b0, F32, "dh0")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,D,layout", [(3000, 64, "mixed"), (600, 37, "mixed"), (2000, 64, "open"), (150, 64, "closed")])
+def test_gates_far_on_either_side(rows, D, layout, dtype):
+    """f up to 20 on either side: 1 - a down to 2e-9, where an fp32 a is 1."""
+    rng = np.random.default_rng(rows + D)
+    f = rng.uniform(-20, 20, size=(rows, D))
+    if layout == "open":
+        f = rng.uniform(8, 20, size=(rows, D))
+    elif layout == "closed":
+        f = rng.uniform(-20, -5, size=(rows, D))
+    both_directions(dtype, "sigmoid", f, [0, rows // 3, rows])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_long_memory_of_open_gates(dtype):
+    """The state follows v by 1 - a a row over tens of thousands of rows."""
+    f = np.broadcast_to(np.array([8.0, 10.0, 12.0, 13.0, 14.0, 15.0, 16.0, 18.0]), (40000, 8)).copy()
+    both_directions(dtype, "sigmoid", f, [0, 40000])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_tokens_continue_a_scan_of_open_gates(dtype):
+    """A prompt in one call and the same tokens one by one end in one state."""
+    f = np.random.default_rng(7).uniform(6, 17, size=(300, 40))
+    (f, v, _, h0, _), (f64, v64, _, h64, _) = operands(dtype, f, 1)
+    _, last = sgr.gated_scan(f, v, h0)
+    state = h0.clone()
+    for t in range(f.shape[0]):
+        sgr.gated_step(f[t:t + 1], v[t:t + 1], state)
+    _, want, _, bound = scan64(f64, v64, h64, [0, f.shape[0]], "sigmoid")
+    check(last, want, bound, F32, "scan")
+    check(state, want, bound, F32, "steps")
