@@ -154,36 +154,36 @@ template <typename IO, class V> __device__ __forceinline__ void open_gate(V p, V
     }
 }
 
-// exp(min(f, 0)).  PRECISE (fp32 I/O): decays near 1 carry a state over
-// thousands of steps, where the MUFU's 2^x would drift (2^-22 a step, not
+// exp(min(f, 0)).  Decays near 1 carry an fp32 state over thousands of steps,
+// whatever the type of f, where the MUFU's 2^x would drift (2^-22 a step, not
 // centred); for f > -1/4 the Taylor series 1 + f + ... + f^7 / 7!, whose rest
 // is below 2^-31, keeps the error at fp32's rounding of a.  Below -1/4 memory
-// is a few steps and the MUFU's error stays where it is.
-template <bool PRECISE>
-__device__ __forceinline__ float log_decay(float f) {
-    const float x = min_nan(f, 0.f);
-    const float far = fast_exp2(x * -kNegLog2e);
-    if constexpr (!PRECISE) return far;
-    float p = 1.f / 5040.f;
-    p = fmaf(p, x, 1.f / 720.f);
-    p = fmaf(p, x, 1.f / 120.f);
-    p = fmaf(p, x, 1.f / 24.f);
-    p = fmaf(p, x, 1.f / 6.f);
-    p = fmaf(p, x, 0.5f);
-    p = fmaf(p, x, 1.f);
-    const float near = fmaf(p, x, 1.f);
-    return x > -0.25f ? near : far;
+// is a few steps and the MUFU's error stays where it is.  Packed for two
+// channels: bf16 32768 x 4096 in 23 sequences 166 us, 186 a channel at a time,
+// 158 by the MUFU alone.
+template <class V> __device__ __forceinline__ V log_decay(V f) {
+    const V x = vmap(f, [](float t) { return min_nan(t, 0.f); });
+    const V far = vmap(vmul(x, vset<V>(-kNegLog2e)), [](float t) { return fast_exp2(t); });
+    V p = vset<V>(1.f / 5040.f);
+    p = vfma(p, x, vset<V>(1.f / 720.f));
+    p = vfma(p, x, vset<V>(1.f / 120.f));
+    p = vfma(p, x, vset<V>(1.f / 24.f));
+    p = vfma(p, x, vset<V>(1.f / 6.f));
+    p = vfma(p, x, vset<V>(0.5f));
+    p = vfma(p, x, vset<V>(1.f));
+    const V near = vfma(p, x, vset<V>(1.f));
+    return vmap(x, near, far, [](float t, float n, float g) { return t > -0.25f ? n : g; });
 }
 
 // (f, v) -> (a, b) of h' = a h + b
-template <int GATE, typename IO, class V>
+template <int GATE, class V>
 __device__ __forceinline__ void gate_pair(V f, V v, V &a, V &b) {
     if constexpr (GATE == GATE_SIGMOID) {
         V z;
         split_small(vmap(f, [](float x) { return signed_small(x); }), a, z);
         b = vmul(z, v);
     } else {
-        a = vmap(f, [](float x) { return log_decay<sizeof(IO) == 4>(x); });
+        a = log_decay(f);
         b = v;
     }
 }

@@ -751,7 +751,7 @@ __device__ __forceinline__ RowReader<IO, E, TMA, R> reader(const GatedParams &p,
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ V fwd_gate(V f) {
     if constexpr (GATE == GATE_LOG) {
-        return vmap(f, [](float x) { return log_decay<sizeof(IO) == 4>(x); });
+        return log_decay(f);
     } else {
         return hold_gate<IO>(f);
     }
@@ -905,11 +905,7 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
 template <int GATE, typename IO, class V>
 __device__ __forceinline__ V bwd_gate(V f) {
     if constexpr (GATE == GATE_SIGMOID) return fwd_gate<GATE, IO>(f);
-    else
-        return vmap(f, [](float x) {
-            const float t = log_decay<sizeof(IO) == 4>(x);
-            return x > 0.f ? -t : t;
-        });
+    else return vmap(log_decay(f), f, [](float t, float x) { return x > 0.f ? -t : t; });
 }
 // (a, z) of it; z is 1 for GATE_LOG
 template <int GATE, typename IO, class V>

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const StepParams p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float a, b;
-                gate_pair<GATE, IO>(f[u].x[i], v[u].x[i], a, b);
+                gate_pair<GATE>(f[u].x[i], v[u].x[i], a, b);
                 st[u].x[i] = fmaf(a, st[u].x[i], b);
             }
             store_values<IO, V>(p.h, r * p.h_rs + d, st[u]);

@@ -100,3 +100,37 @@ def test_tokens_continue_a_scan_of_open_gates(dtype):
     _, want, _, bound = scan64(f64, v64, h64, [0, f.shape[0]], "sigmoid")
     check(last, want, bound, F32, "scan")
     check(state, want, bound, F32, "steps")
+
+
+# ------------------------------------------------------ decays next to 1
+#
+# With v = 0, h0 = 1 and one row the fp32 state is the decay itself.  For
+# -1/4 < f <= 0 its series ends in p = 1 + x (...) and 1 + x p: p is off by
+# less than 2^-24 (a rounding below 1 is 2^-25, those before it come in times
+# |x| / 2), so x p by less than 2^-26, and the last rounding is 2^-25; the terms
+# left out are below 2^-31.  Together less than 2^-24.
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_decays_next_to_one_are_rounded_once(dtype):
+    x = torch.cat([torch.linspace(-0.2499, 0, 4000), -torch.logspace(-7, -0.61, 4000)])
+    f = x.to(dtype).to(DEV).view(-1, 8)
+    zero, one = torch.zeros_like(f), torch.ones(f.shape[0], 8, device=DEV)
+    want = np.exp(f.double().cpu().numpy())
+    _, last = sgr.gated_scan(f, zero, one, torch.arange(f.shape[0] + 1, device=DEV), "log")
+    state = one.clone()
+    sgr.gated_step(f, zero, state, gate="log")
+    for got in (last, state):
+        assert np.abs(got.double().cpu().numpy() - want).max() < 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_long_memory_of_log_gates(dtype):
+    f = np.broadcast_to(-np.exp2(-np.arange(2.0, 18.0, 2.0)), (40000, 8)).copy()
+    both_directions(dtype, "log", f, [0, 40000])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,D", [(3000, 64), (600, 37)])
+def test_log_gates_of_many_sizes(rows, D, dtype):
+    rng = np.random.default_rng(rows)
+    f = -np.exp(rng.uniform(-10, 4, size=(rows, D))) * np.where(rng.random((rows, D)) < 0.1, -1, 1)
+    both_directions(dtype, "log", f, [0, rows // 3, rows])
