@@ -918,6 +918,14 @@ __device__ __forceinline__ void bwd_split(V s, V &a, V &z) {
     }
 }
 
+// df of a row from c = a z (h - v) or a h: where f > 0 it is 0, whatever c and
+// g are (a product would make NaN of an infinite one).
+template <int GATE, class V> __device__ __forceinline__ V bwd_df(V s, V c, V g) {
+    const V y = vmul(c, g);
+    if constexpr (GATE == GATE_SIGMOID) return y;
+    else return vmap(s, y, [](float t, float u) { return is_cut(t) ? 0.f : u; });
+}
+
 template <typename IO, int E, bool TMA> struct BackwardShape {
     using Ring = SmemShape<IO, E, 3, kBwdSlots, kBwdTR, TMA>;
     using Blk = Block<typename FVec<E>::type, kBwdSlots, kBwdTR, 2>;            // maps 0: reverse, 1: forward
@@ -1027,7 +1035,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                         c[r] = vmul(vmul(a, z), vfma(x, vset<V>(-1.f), h));
                         h = vfma(a, h, vmul(z, x));
                     } else {
-                        c[r] = vmap(s[r], h, [](float y, float w) { return is_cut(y) ? 0.f : y * w; });
+                        c[r] = vmul(s[r], h);
                         h = vfma(a, h, x);
                     }
                 }
@@ -1045,7 +1053,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                     V a, z;
                     bwd_split<GATE, IO>(s[r], a, z);
                     if (dvalid) {
-                        __stcs(reinterpret_cast<W *>(pf), C::out(vmul(c[r], g)));
+                        __stcs(reinterpret_cast<W *>(pf), C::out(bwd_df<GATE>(s[r], c[r], g)));
                         __stcs(reinterpret_cast<W *>(pv), C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g));
                     }
                     pf -= pitch_f;
@@ -1061,7 +1069,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                     bwd_split<GATE, IO>(s[r], a, z);
                     if (dvalid && row + r < info.row_end) {
                         const bool live = k.z >> r & 1u;
-                        __stcs(reinterpret_cast<W *>(pf), live ? C::out(vmul(c[r], g)) : W(0));
+                        __stcs(reinterpret_cast<W *>(pf), live ? C::out(bwd_df<GATE>(s[r], c[r], g)) : W(0));
                         __stcs(reinterpret_cast<W *>(pv), live ? C::out(GATE == GATE_SIGMOID ? vmul(z, g) : g) : W(0));
                     }
                     pf -= pitch_f;

@@ -134,3 +134,31 @@ def test_log_gates_of_many_sizes(rows, D, dtype):
     rng = np.random.default_rng(rows)
     f = -np.exp(rng.uniform(-10, 4, size=(rows, D))) * np.where(rng.random((rows, D)) < 0.1, -1, 1)
     both_directions(dtype, "log", f, [0, rows // 3, rows])
+
+
+# --------------------------------------- a gate without gradient (f > 0)
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows", [5, 500])
+def test_no_gradient_where_the_log_gate_is_clamped(rows, dtype):
+    """df = [f <= 0] a h g is 0 where f > 0, also beside a state or an
+    upstream gradient that is infinite or NaN."""
+    torch.manual_seed(rows)
+    f = torch.randn(rows, 6, device=DEV).abs().neg()
+    f[::3] = 0.5
+    v, dh = torch.randn(rows, 6, device=DEV), torch.randn(rows, 6, device=DEV)
+    inf, nan = float("inf"), float("nan")
+    last = rows - rows % 3 - (3 if rows % 3 == 0 else 0)      # the last clamped row
+    v[0, 1], v[0, 2] = inf, nan                               # in the state from there on
+    dh[last, 3], dh[last, 4], dh[last, 5] = inf, nan, -inf    # in the flow up to there
+    f, v, dh = f.to(dtype), v.to(dtype), dh.to(dtype)
+    _, _, states = sgr.gated_scan(f, v, gate="log", save_states=True)
+    df, dv, _ = sgr.gated_scan_backward(f, v, None, states, dh, gate="log")
+    assert bool((df[f > 0] == 0).all())
+    # with no clamped row the same infinities do reach df
+    g = torch.minimum(f, torch.zeros_like(f))
+    _, _, states = sgr.gated_scan(g, v, gate="log", save_states=True)
+    df0, dv0, _ = sgr.gated_scan_backward(g, v, None, states, dh, gate="log")
+    assert bool((~torch.isfinite(df0[1:last + 1, 1:])).any(0).all()) and torch.equal(dv.isnan(), dv0.isnan())
+    bad = torch.full_like(f, nan)                             # a gate that is NaN itself
+    df, _, _ = sgr.gated_scan_backward(bad, v, None, states, dh, gate="log")
+    assert bool(df[1:].isnan().all())
