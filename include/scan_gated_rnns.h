@@ -579,6 +579,9 @@ SGR_API int sgr_backward_kernel(sgr_op_t op, int64_t B, int64_t T, int64_t D, sg
  *   chain) skips publishing its state, so the chunk after it in the same
  *   channels waits until the limit, records SGR_ERR_TIMEOUT in the workspace
  *   status word and writes NaN for its outputs; -1 (the default) disables it.
+ *   In gated_scan chunks count 192 rows, in its gradient 96 rows from the end,
+ *   within each of the segments that the sequences fall into, and chains are
+ *   128 bytes of a row.
  */
 SGR_API sgr_status_t sgr_set_wait_limit(uint32_t polls);
 SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
@@ -617,8 +620,9 @@ SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
  * States and arithmetic are fp32.  A NaN or infinity stays within its sequence
  * and channel (behind an infinite state the sequence holds infinities or NaN).  The result does not depend on how blocks are timed: equal
  * calls give equal bits.  Calls may be captured.  A chunk that waited too long
- * leaves NaN and sets the workspace's first word to SGR_ERR_TIMEOUT (~0
- * otherwise, behind a call that needs a workspace).
+ * for an earlier one (sgr_set_wait_limit) leaves NaN in the rest of its channels'
+ * segment and sets the workspace's first word to SGR_ERR_TIMEOUT; a call that
+ * needs a workspace clears the word first, and sgr_workspace_status reads it.
  */
 SGR_API sgr_status_t gated_scan(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride,
                                 const float *h0, int64_t h0_seq_stride, const void *cu_seqlens, int cu_bytes,

@@ -22,7 +22,8 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1 - kTR;
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Workspace: header, then the words through which tiles hand their maps and
-// final states on.  Every byte is set to ~0 on the stream before the launch.
+// final states on.  All of it is set to ~0, the status word to 0, on the
+// stream before the launch.
 // The rows fall into segments, each of whole chunks, so up to segs - 1 chunks
 // come on top of the rows' own.
 struct Layout {
@@ -182,7 +183,8 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
     const Layout l = layout(p.rows, p.D, 32 * E, tr, p.n_segs);
     p.n_strips = l.n_strips;
     p.seq_rows = p.cu ? 1u : uint32_t(p.rows / std::max<int64_t>(1, p.n_seqs));
-    p.spin_limit = kSpinLimit;
+    p.spin_limit = host::wait_limit();
+    p.drop_tile = host::drop_tile();
     Span out[4], in[8];
     if (backward) {
         out[0] = {p.df, b_df};

@@ -92,8 +92,9 @@ struct GatedParams {
     int zero_padding;                      // outputs of rows in no sequence: 0 written, else left
     uint64_t *words;                       // [chunks][n_strips][TC] what tiles hand on, ~0 at launch
     uint32_t *ticket;                      // ~0 at launch, or null: one chunk, tile = blockIdx.x
-    uint32_t *status;                      // ~0 at launch; SGR_ERR_TIMEOUT once a wait ran out; may be null
-    uint32_t spin_limit;
+    uint32_t *status;                      // 0 at launch; SGR_ERR_TIMEOUT once a wait ran out; may be null
+    uint32_t spin_limit;                   // polls of a look-back
+    int64_t drop_tile;                     // testing: the tile of these words (word * n_strips + strip) hands nothing on
     int window;                            // chunks of a strip and segment that blocks may hold at a time
 };
 
@@ -246,20 +247,20 @@ template <int E> __device__ __forceinline__ void apply_words(const uint64_t (&m)
 }
 
 // The carry of one tile (carry warp): q its place in processing order within
-// its segment, word that of its words, tot the tile's maps of this lane's E
-// channels.  Publishes, waits, and returns the entering states.  Tiles whose
-// first row (in processing order) is a start enter with 0, which they never
-// use.  One round trip reads the words of the kNear tiles before for every
-// channel, and those of up to 32 more for the strip's first channel; if the
-// state is among the far ones, a second round trip reads the rest of the
-// channels.  No word is read that lies further back than the blocks can hold
-// tiles of the strip (p.window), and where those are few the first round
-// reads the tile before alone: an older word has left L2 for memory, and a
-// load from there, behind the streams, took 2.7 us.  `meanwhile` runs under
-// the first round.
+// its segment, word that of its words, mute: it hands nothing on, tot the
+// tile's maps of this lane's E channels.  Publishes, waits, and returns the
+// entering states.  Tiles whose first row (in processing order) is a start
+// enter with 0, which they never use.  One round trip reads the words of the
+// kNear tiles before for every channel, and those of up to 32 more for the
+// strip's first channel; if the state is among the far ones, a second round
+// trip reads the rest of the channels.  No word is read that lies further back
+// than the blocks can hold tiles of the strip (p.window), and where those are
+// few the first round reads the tile before alone: an older word has left L2
+// for memory, and a load from there, behind the streams, took 2.7 us.
+// `meanwhile` runs under the first round.
 constexpr int kNear = 4;
 template <int E, class Meanwhile>
-__device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int q, int word, bool last, int lane,
+__device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t strip, int q, int word, bool mute, int lane,
                                                  bool fresh, bool cut, const float2 (&tot)[E], float (&hin)[E],
                                                  Meanwhile meanwhile) {
     constexpr int TC = 32 * E;
@@ -268,7 +269,7 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
 #pragma unroll
     for (int e = 0; e < E; ++e) hin[e] = 0.f;
     auto publish_state = [&] {
-        if (last) return;
+        if (mute) return;
 #pragma unroll
         for (int e = 0; e < E; ++e) st_relaxed_u64(p.words + at + e, word_of(-0.f, apply_map(tot[e].x, tot[e].y, hin[e])));
     };
@@ -279,7 +280,7 @@ __device__ __forceinline__ void carry_tile_state(const GatedParams &p, int64_t s
     }
     if (cut) {                                                     // a start within: the state does not depend on what enters
         publish_state();
-    } else if (!last) {
+    } else if (!mute) {
 #pragma unroll
         for (int e = 0; e < E; ++e) st_relaxed_u64(p.words + at + e, word_of(tot[e].x, tot[e].y));
     }
@@ -390,10 +391,11 @@ __device__ __forceinline__ void put_state_row(float *base, int64_t off, int64_t 
 // words are: whoever touches the workspace waits here first.
 __device__ __forceinline__ void workspace_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// All of it to ~0, but the status word (the first) to 0.
 __global__ void __launch_bounds__(256) gated_clear_kernel(uint4 *p, int64_t n) {
     asm volatile("griddepcontrol.launch_dependents;");
     for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256)
-        p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+        p[i] = make_uint4(i ? ~0u : 0u, ~0u, ~0u, ~0u);
 }
 
 // ------------------------------------------------------ inside a block
@@ -650,6 +652,7 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
         const int64_t strip = info.strip, state = info.state_row;
         const int q = info.place, word = info.word;
         const bool fresh = q == 0 || (DIR > 0 ? info.start[0] : info.end[TR - 1]) >= 0, last = info.last;
+        const bool mute = last || int64_t(word) * p.n_strips + strip == p.drop_tile;
         const bool halves = info.row0 + kBwdTR < info.row_end;
         const bool cut = info.cut & (DIR > 0 ? 1 : 2), begins = info.cut & 1;
         const int e0 = n % kQ;
@@ -679,7 +682,7 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
 #pragma unroll
         for (int e = 0; e < E; ++e)
             tot[e] = make_float2(reinterpret_cast<const float *>(&tA)[e], reinterpret_cast<const float *>(&tB)[e]);
-        carry_tile_state<E>(p, strip, q, word, last, lane, fresh, cut, tot, hin, [&] {
+        carry_tile_state<E>(p, strip, q, word, mute, lane, fresh, cut, tot, hin, [&] {
             if constexpr (DIR < 0) {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {

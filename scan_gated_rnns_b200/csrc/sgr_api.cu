@@ -2,6 +2,7 @@
 // argument checks, the choice of chunk shape, the workspace layout and the
 // kernel launches.  No allocation, no synchronisation on the scan paths.
 #include "scan_gated_rnns.h"
+#include "host_checks.h"
 #include "projected_scan.cuh"
 #include "scan_backward.cuh"
 #include "scan_engine.cuh"
@@ -1586,6 +1587,9 @@ sgr_status_t run_projected_scan(const void *x, const void *w, const float *h0, i
 }
 
 }  // namespace
+
+uint32_t sgr::host::wait_limit() { return g_spin_limit.load(); }
+int64_t sgr::host::drop_tile() { return g_drop_tile.load(); }
 
 extern "C" {
 

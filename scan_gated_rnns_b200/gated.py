@@ -126,10 +126,14 @@ def _sizes(rows: int, D: int) -> Tuple[int, int]:
     return int(lib().sgr_gated_workspace_size(rows, D)), int(lib().sgr_gated_chunks(rows))
 
 
-def _scratch(need: int, device) -> Optional[torch.Tensor]:
-    """The call's own workspace: of the caching allocator, so that calls on
-    other streams and captured graphs each have theirs."""
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+def _scratch(need: int, device, workspace: Optional[ops.Workspace]) -> Optional[torch.Tensor]:
+    """The workspace given, or the call's own: of the caching allocator, so that
+    calls on other streams and captured graphs each have theirs."""
+    if workspace is None or not need:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if workspace.nbytes < need or workspace.buf.device != device:
+        raise ValueError(f"workspace must hold {need} bytes on {device}")
+    return workspace.buf
 
 
 class _Call(NamedTuple):
@@ -155,11 +159,11 @@ def _call(fn: str, f: torch.Tensor, v: torch.Tensor, cu: Optional[torch.Tensor],
     return _Call(g, dt, f_rs, v_rs, rows, D, n, cb, *_sizes(rows, D))
 
 
-def _forward(c: _Call, f, v, hp, hss, cu, out, o_rs, zero, save_states):
+def _forward(c: _Call, f, v, hp, hss, cu, out, o_rs, zero, save_states, workspace=None):
     device = f.device
     h_last = torch.empty((c.n, c.D), dtype=torch.float32, device=device)
     states = torch.empty((c.chunks, c.D), dtype=torch.float32, device=device) if save_states else None
-    ws = _scratch(c.need, device)
+    ws = _scratch(c.need, device, workspace)
     code = _launch(lib().gated_scan, device.index, f.data_ptr(), c.f_rs, v.data_ptr(), c.v_rs, hp, hss,
                    cu.data_ptr() if c.cu_bytes else 0, c.cu_bytes, c.n, out.data_ptr(), o_rs, h_last.data_ptr(),
                    states.data_ptr() if save_states else 0, c.rows, c.D, c.gate, c.dtype, zero,
@@ -168,11 +172,11 @@ def _forward(c: _Call, f, v, hp, hss, cu, out, o_rs, zero, save_states):
     return h_last, states
 
 
-def _backward(c: _Call, f, v, hp, hss, cu, states, dh, dh_rs, lp, want_dh0):
+def _backward(c: _Call, f, v, hp, hss, cu, states, dh, dh_rs, lp, want_dh0, workspace=None):
     device = f.device
     df, dv = _dense(f), _dense(f)
     dh0 = torch.empty((c.n, c.D), dtype=torch.float32, device=device) if want_dh0 else None
-    ws = _scratch(c.need, device)
+    ws = _scratch(c.need, device, workspace)
     code = _launch(lib().gated_scan_backward, device.index, f.data_ptr(), c.f_rs, v.data_ptr(), c.v_rs, hp, hss,
                    cu.data_ptr() if c.cu_bytes else 0, c.cu_bytes, c.n, states.data_ptr(), dh.data_ptr(), dh_rs, lp,
                    df.data_ptr(), c.D, dv.data_ptr(), c.D, dh0.data_ptr() if want_dh0 else 0, c.rows, c.D, c.gate,
@@ -183,7 +187,8 @@ def _backward(c: _Call, f, v, hp, hss, cu, states, dh, dh_rs, lp, want_dh0):
 
 def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = None,
                cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid",
-               out: Optional[torch.Tensor] = None, save_states: bool = False):
+               out: Optional[torch.Tensor] = None, save_states: bool = False,
+               workspace: Optional[ops.Workspace] = None):
     """(h, h_last): the gated linear recurrence over f, v, (B, T, D) or, with
     cu_seqlens, packed rows (N, D); float32, bfloat16 or float16, rows of any
     even spacing (the halves of one projection are read in place).
@@ -192,7 +197,12 @@ def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = No
     empty, and rows outside [cu[0], cu[-1]) are padding: 0 in the result, left
     as they were in a given ``out``.  h0: float32 (S, D), or (D,) for every
     sequence.  h_last: float32 (S, D), the state behind each sequence.  With
-    save_states a third result: what gated_scan_backward starts from."""
+    save_states a third result: what gated_scan_backward starts from.
+
+    A wait between blocks that runs out leaves NaN.  With a workspace of
+    workspace_size("gated", ...) bytes, which only one call at a time may use
+    and only scans of this kind, its status() then says so; without one each
+    call takes its own."""
     fn = "gated_scan"
     c = _call(fn, f, v, cu_seqlens, gate)
     hp, hss = _states(h0, c.n, c.D, f, fn + ": h0", True)
@@ -201,16 +211,19 @@ def gated_scan(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor] = No
         out = _dense(f)
     else:
         o_rs = _operand(out, f, fn + ": out")
-    h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, out, o_rs, int(zero), save_states)
+    h_last, states = _forward(c, f, v, hp, hss, cu_seqlens, out, o_rs, int(zero), save_states,
+                              workspace)
     return (out, h_last, states) if save_states else (out, h_last)
 
 
 def gated_scan_backward(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Tensor], states: torch.Tensor,
                         dh: torch.Tensor, dh_last: Optional[torch.Tensor] = None,
-                        cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid", want_dh0: bool = True):
+                        cu_seqlens: Optional[torch.Tensor] = None, gate: str = "sigmoid", want_dh0: bool = True,
+                        workspace: Optional[ops.Workspace] = None):
     """(df, dv, dh0) for dL/dh = dh and dL/dh_last = dh_last through
     h, h_last, states = gated_scan(f, v, h0, cu_seqlens, gate, save_states=True);
-    dh0 is float32 (S, D), one row per sequence (None unless want_dh0)."""
+    dh0 is float32 (S, D), one row per sequence (None unless want_dh0).  workspace
+    as for gated_scan."""
     fn = "gated_scan_backward"
     c = _call(fn, f, v, cu_seqlens, gate)
     dh_rs = _operand(dh, f, fn + ": dh")
@@ -221,7 +234,7 @@ def gated_scan_backward(f: torch.Tensor, v: torch.Tensor, h0: Optional[torch.Ten
     _, sss = _states(states, c.chunks, c.D, f, fn + ": states", False)
     if states is None or (c.chunks > 1 and sss != c.D):
         raise ValueError(f"{fn}: states must be the contiguous ({c.chunks}, {c.D}) tensor that gated_scan saved")
-    return _backward(c, f, v, hp, hss, cu_seqlens, states, dh, dh_rs, lp, want_dh0)
+    return _backward(c, f, v, hp, hss, cu_seqlens, states, dh, dh_rs, lp, want_dh0, workspace)
 
 
 class GatedScan(torch.autograd.Function):

@@ -84,6 +84,10 @@ _cache = {}
 
 
 def workspace_size(op: str, B: int, T: int, D: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace of a scan of (B, T, D); "gated": of gated_scan and its
+    gradient, whose packed rows count as one sequence."""
+    if op == "gated":
+        return int(lib().sgr_gated_workspace_size(B * T, D))
     opc = {"mingru": _abi.SGR_OP_MINGRU, "minmax": _abi.SGR_OP_MINMAX, "mingru_log": _abi.SGR_OP_MINGRU_LOG}[op]
     return int(lib().sgr_workspace_size(opc, B, T, D, _DT[dtype]))
 

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import scan_gated_rnns_b200 as sgr
+from scan_gated_rnns_b200 import _abi
 
 from gated_reference import check, grad64, scan64
 
@@ -162,3 +163,72 @@ def test_no_gradient_where_the_log_gate_is_clamped(rows, dtype):
     bad = torch.full_like(f, nan)                             # a gate that is NaN itself
     df, _, _ = sgr.gated_scan_backward(bad, v, None, states, dh, gate="log")
     assert bool(df[1:].isnan().all())
+
+
+# ------------------------------------------------------ waits that run out
+@pytest.fixture
+def hooks():
+    lib = _abi.lib()
+    yield lib
+    lib.sgr_set_wait_limit(0)
+    lib.sgr_set_drop_publish(-1)
+
+
+def compare(got, want, clean, name):
+    """NaN outside `clean` (a mask of rows and channels), the same bits in it."""
+    got, want = (x.reshape(clean.shape) for x in (got, want))
+    assert bool(got[~clean].isnan().all()) and torch.equal(got[clean], want[clean]), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", ["sigmoid", "log"])
+def test_a_tile_that_hands_nothing_on(gate, dtype, hooks):
+    """The first tile of the first channels is mute: the tiles behind it give
+    up, say so and give NaN up to the next sequence; the rest is as it was, and
+    so is the next call."""
+    rows, D, cu, strip = 2000, 160, [0, 500, 2000], 128 // dtype.itemsize
+    rng = np.random.default_rng(1)
+    f = rng.normal(size=(rows, D)) + 1 if gate == "sigmoid" else -np.exp(rng.normal(size=(rows, D)))
+    (f, v, dh, h0, dl), _ = operands(dtype, f, 2, 2)
+    cu_d = torch.tensor(cu, device=DEV)
+    ws = sgr.Workspace(sgr.workspace_size("gated", 1, rows, D, dtype), DEV)
+    clean = sgr.gated_scan(f, v, h0, cu_d, gate, save_states=True, workspace=ws)
+    back = sgr.gated_scan_backward(f, v, h0, clean[2], dh, dl, cu_d, gate, workspace=ws)
+    assert ws.status() == 0
+    hooks.sgr_set_wait_limit(500)
+    hooks.sgr_set_drop_publish(0)
+    h, last = sgr.gated_scan(f, v, h0, cu_d, gate, workspace=ws)
+    assert ws.status(clear=False) == _abi.SGR_ERR_TIMEOUT
+    ok = torch.ones(rows, D, dtype=torch.bool, device=DEV)
+    ok[192:500, :strip] = False
+    compare(h, clean[0], ok, "h")
+    ok = torch.ones(2, D, dtype=torch.bool, device=DEV)
+    ok[0, :strip] = False
+    compare(last, clean[1], ok, "h_last")
+    df, dv, d0 = sgr.gated_scan_backward(f, v, h0, clean[2], dh, dl, cu_d, gate, workspace=ws)
+    assert ws.status() == _abi.SGR_ERR_TIMEOUT and ws.status() == 0
+    ok = torch.ones(rows, D, dtype=torch.bool, device=DEV)
+    ok[500:1920, :strip] = False                             # 96 rows a tile: the last of them begins at 1920
+    compare(df, back[0], ok, "df")
+    compare(dv, back[1], ok, "dv")
+    ok = torch.ones(2, D, dtype=torch.bool, device=DEV)
+    ok[1, :strip] = False
+    compare(d0, back[2], ok, "dh0")
+    hooks.sgr_set_drop_publish(-1)
+    hooks.sgr_set_wait_limit(0)
+    for a, b in zip(sgr.gated_scan(f, v, h0, cu_d, gate, workspace=ws), clean):
+        assert torch.equal(a, b)
+    for a, b in zip(sgr.gated_scan_backward(f, v, h0, clean[2], dh, dl, cu_d, gate, workspace=ws), back):
+        assert torch.equal(a, b)
+    assert ws.status() == 0
+
+
+def test_workspaces_that_do_not_fit():
+    f = torch.zeros(1000, 64, device=DEV)
+    need = sgr.workspace_size("gated", 1, 1000, 64, F32)
+    assert need == sgr.workspace_size("gated", 10, 100, 64, F32)
+    with pytest.raises(ValueError, match="workspace"):
+        sgr.gated_scan(f, f, workspace=sgr.Workspace(need - 16, DEV))
+    with pytest.raises(ValueError, match="workspace"):
+        sgr.gated_scan(f, f, workspace=sgr.Workspace(need, "cpu"))
+    assert torch.equal(sgr.gated_scan(f[:50], f[:50], workspace=sgr.Workspace(16, DEV))[0], f[:50])   # needs none
