@@ -571,10 +571,15 @@ SGR_API int sgr_backward_kernel(sgr_op_t op, int64_t B, int64_t T, int64_t D, sg
 /* ------------------------------------------------------- testing hooks */
 
 /*
- * Both hooks are process-wide and exist to exercise the bounded wait of the
+ * These hooks are process-wide and exist to exercise the bounded waits of the
  * chunk hand-off without faulting or hanging a GPU.
  * sgr_set_wait_limit: polls a chunk makes before it gives up waiting for an
  *   earlier chunk (0 restores the default of 2^18 polls, a fraction of a second).
+ * sgr_set_block_wait_limit: polls, of some microseconds, of gated_scan's and its
+ *   gradient's waits between the warps of a block (0: twice the number of the
+ *   other hook).  One that runs out makes its block give up: what that block
+ *   had not finished, and the chunks it draws from then on, become NaN, and the
+ *   workspace's first word SGR_ERR_TIMEOUT.
  * sgr_set_drop_publish: the block with this tile index (chunk * n_chains +
  *   chain) skips publishing its state, so the chunk after it in the same
  *   channels waits until the limit, records SGR_ERR_TIMEOUT in the workspace
@@ -584,6 +589,7 @@ SGR_API int sgr_backward_kernel(sgr_op_t op, int64_t B, int64_t T, int64_t D, sg
  *   128 bytes of a row.
  */
 SGR_API sgr_status_t sgr_set_wait_limit(uint32_t polls);
+SGR_API sgr_status_t sgr_set_block_wait_limit(uint32_t polls);
 SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
 
 /* ------------------------------------------ gated linear recurrence */

@@ -72,6 +72,7 @@ SIGNATURES.update({
     "sgr_scan_plan": (_int, [_int, _i64, _i64, _i64, _int, _int, ctypes.POINTER(Plan)]),
     "sgr_scan_plan_decay": (_int, [_i64, _i64, _i64, _int, _int, ctypes.POINTER(Plan)]),
     "sgr_set_wait_limit": (_int, [ctypes.c_uint32]),
+    "sgr_set_block_wait_limit": (_int, [ctypes.c_uint32]),
     "sgr_set_drop_publish": (_int, [_i64]),
     "sgr_set_kernel_override": (_int, [_int]),
     "sgr_backward_kernel": (_int, [_int, _i64, _i64, _i64, _int, _int]),

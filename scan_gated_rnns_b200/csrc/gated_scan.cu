@@ -185,6 +185,7 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
     p.seq_rows = p.cu ? 1u : uint32_t(p.rows / std::max<int64_t>(1, p.n_seqs));
     p.spin_limit = host::wait_limit();
     p.drop_tile = host::drop_tile();
+    p.tile_wait = host::block_wait_limit() ? host::block_wait_limit() : 2 * std::min(p.spin_limit, uint32_t(1) << 30);
     Span out[4], in[8];
     if (backward) {
         out[0] = {p.df, b_df};

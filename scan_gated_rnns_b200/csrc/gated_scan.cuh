@@ -67,7 +67,7 @@ constexpr int kTR = kWarps * kRows;        // rows per forward tile
 constexpr int kBwdTR = kWarps * kBwdRows;  // rows per backward tile, and between saved states
 constexpr int kSlots = 4, kBwdSlots = 5;   // tiles in shared memory
 constexpr int kQ = 2;                      // tiles between fold and the end of their replay
-constexpr uint32_t kTileWait = 1u << 16;   // polls of a wait inside the block (each suspends for tens of us)
+constexpr uint32_t kCopyWait = 1u << 16;   // polls, of about 4 us, of a lost block for its copies in flight
 static_assert(kTR == 2 * kBwdTR, "a forward tile holds two saved states");
 constexpr int kSegs = 32;                  // most segments: one per lane of the feeding warp
 constexpr uint64_t kNone = ~uint64_t(0);    // a word not yet published
@@ -93,7 +93,8 @@ struct GatedParams {
     uint64_t *words;                       // [chunks][n_strips][TC] what tiles hand on, ~0 at launch
     uint32_t *ticket;                      // ~0 at launch, or null: one chunk, tile = blockIdx.x
     uint32_t *status;                      // 0 at launch; SGR_ERR_TIMEOUT once a wait ran out; may be null
-    uint32_t spin_limit;                   // polls of a look-back
+    uint32_t spin_limit;                   // polls of a look-back, one to three us each
+    uint32_t tile_wait;                    // polls, of about 4 us, of a wait inside a block
     int64_t drop_tile;                     // testing: the tile of these words (word * n_strips + strip) hands nothing on
     int window;                            // chunks of a strip and segment that blocks may hold at a time
 };
@@ -403,8 +404,14 @@ __global__ void __launch_bounds__(256) gated_clear_kernel(uint4 *p, int64_t n) {
 // Tile n of the block lies in slot n % S from its copies until every data
 // warp has replayed it; its maps and entering states in entry n % kQ: a data
 // warp folds tile n after its replay of tile n - 2, which it began with that
-// tile's states.  Every wait is bounded; one that runs out poisons the tile
-// (NaN) and records it, and nothing else waits on it.
+// tile's states.  Every wait is bounded.  Each of these depends, through a
+// warp or two of the block, on at most one look-back that may run to its own
+// end, so their bound is twice as many polls, each longer.  Should one run
+// out all the same, the block is lost: a warp whose wait failed leaves its loop
+// without an arrival, so that no barrier ever counts a phase that did not
+// happen and a wait that succeeds has found what it waited for; once all have
+// left, the block writes NaN for every tile it had not finished and for those
+// it can still draw, and hands NaN on (give_up).
 template <typename V, int S, int TR, int MAPS> struct Block {
     uint64_t full[S], empty[S];            // copies and table there; replayed by every data warp
     uint64_t maps[kQ], in[kQ];             // maps there; entering states there
@@ -415,6 +422,9 @@ template <typename V, int S, int TR, int MAPS> struct Block {
     V A[MAPS][kQ][kWarps][32], B[MAPS][kQ][kWarps][32];
     V enter[kQ][32];                       // states entering the tile
     int bounds[kBoundsHeld];
+    int lost;                              // a wait ran out
+    int fed, done[kWarps];                 // tiles handed over; replayed by each data warp (at its end)
+    uint32_t ticket;                       // the feeding warp's last, in hand or behind the end
 };
 template <int S, class B> __device__ __forceinline__ void init_block(B &blk) {
     if (threadIdx.x == 0) {
@@ -426,6 +436,7 @@ template <int S, class B> __device__ __forceinline__ void init_block(B &blk) {
             mbar_init(smem_addr(&blk.maps[i]), kWarps);
             mbar_init(smem_addr(&blk.in[i]), 1);
         }
+        blk.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -433,15 +444,22 @@ template <int S, class B> __device__ __forceinline__ void init_block(B &blk) {
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// wait for use u of a barrier (its phases are uses 0, 1, 2, ...)
+// Wait of a warp for use u of a barrier (its phases are uses 0, 1, 2, ...), all
+// lanes together: the result is the warp's.  (Lanes that poll by themselves and
+// vote behind it: 189 us for bf16 32768 x 4096 forward, 186 so.)
 struct Waiter {
-    uint32_t *status;
+    int *lost;
     uint32_t limit;
-    __device__ __forceinline__ bool operator()(uint64_t *bar, int u) {
-        if (mbar_wait(smem_addr(bar), uint32_t(u & 1), limit)) return true;
-        limit = 1;
-        if (status) atomicExch(status, 5u);                           // SGR_ERR_TIMEOUT
-        return false;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, int u) const {
+        const uint32_t at = smem_addr(bar), phase = uint32_t(u & 1);
+        bool ok = mbar_try_wait(at, phase);
+        if (__builtin_expect(__all_sync(0xffffffffu, ok), 1)) return true;
+        uint32_t polls = 1;
+        do {
+            ok = __all_sync(0xffffffffu, mbar_try_wait(at, phase));
+        } while (!ok && ++polls < limit);
+        if (!ok) *lost = 1;
+        return ok;
     }
 };
 __device__ __forceinline__ float nan_value() { return __int_as_float(0x7fffffff); }
@@ -537,14 +555,48 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
 }
 
+// The tile of a ticket (whole warp); false behind the last.  `reverse`: places
+// count from the segment's end.
+template <int TR> struct TileAt {
+    int64_t row0, row_end;
+    int strip, place, word, state, last;
+
+    __device__ __forceinline__ bool find(const GatedParams &p, Segments<TR> &seg, uint32_t tile, int lane, bool reverse) {
+        const uint32_t k = tile / uint32_t(p.n_strips);
+        const bool there = k < uint32_t(seg.total);
+        int g = 0;
+        if (there) g = seg.find(int(k), lane);
+        const int count = __shfl_sync(0xffffffffu, seg.n, g);
+        const int c = reverse ? count - 1 - seg.c : seg.c;                      // chunk of the segment
+        const int64_t from = __shfl_sync(0xffffffffu, seg.start, g), end = from + __shfl_sync(0xffffffffu, seg.len, g);
+        strip = int(tile - k * uint32_t(p.n_strips));
+        place = seg.c;
+        word = __shfl_sync(0xffffffffu, seg.word0, g) + seg.c;
+        state = __shfl_sync(0xffffffffu, seg.state0, g) + c * (TR / kBwdTR);
+        last = seg.c + 1 == count;
+        row0 = from + int64_t(c) * TR;
+        row_end = row0 + TR < end ? row0 + TR : end;
+        return there;
+    }
+    __device__ __forceinline__ void put(TileInfo<TR> &info) const {
+        info.row0 = row0;
+        info.row_end = row_end;
+        info.state_row = state;
+        info.strip = strip;
+        info.place = place;
+        info.word = word;
+        info.last = last;
+    }
+};
+
 // The feeding warp: draws tickets, starts the copies of a tile when its slot
-// is free, writes its table and hands both over.  `reverse`: places count
-// from the segment's end.  Ends with one entry for each carry warp that says
-// so, so that each of them comes upon one.
+// is free, writes its table and hands both over.  Ends with one entry for each
+// carry warp that says so, so that each of them comes upon one; a lost block's
+// when its copies in flight have landed.
 template <int S, int OPS, int TR, uint32_t OP_BYTES, int TC, bool TMA, class B>
 __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slots, int lane, bool reverse,
                                      const CUtensorMap *m0, const CUtensorMap *m1, const CUtensorMap *m2) {
-    Waiter wait{p.status, kTileWait};
+    const Waiter wait{&blk.lost, p.tile_wait};
     const bool held = p.cu != nullptr && p.n_seqs < kBoundsHeld;
     if (held)
         for (int i = lane; i <= int(p.n_seqs); i += 32) blk.bounds[i] = cu_at(p, i);
@@ -562,20 +614,11 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
     }
     uint64_t once;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-    int ends = 0;
-    for (int n = 0; ends < kCarryWarps; ++n) {
-        const uint32_t tile = __shfl_sync(0xffffffffu, ticket, 0);
-        const uint32_t k = tile / uint32_t(p.n_strips), strip = tile - k * uint32_t(p.n_strips);
-        const bool more = ends == 0 && k < uint32_t(seg.total);
-        int g = 0;
-        if (more) g = seg.find(int(k), lane);
-        const int count = __shfl_sync(0xffffffffu, seg.n, g);
-        const int c = reverse ? count - 1 - seg.c : seg.c;                      // chunk of the segment
-        const int64_t from = __shfl_sync(0xffffffffu, seg.start, g), len = __shfl_sync(0xffffffffu, seg.len, g);
-        const int word = __shfl_sync(0xffffffffu, seg.word0, g) + seg.c;
-        const int state = __shfl_sync(0xffffffffu, seg.state0, g) + c * (TR / kBwdTR);
-        const int64_t row0 = from + int64_t(c) * TR, end = from + len, row_end = row0 + TR < end ? row0 + TR : end;
-        if (n >= S) wait(&blk.empty[n % S], n / S - 1);
+    int ends = 0, n = 0;
+    for (; ends < kCarryWarps; ++n) {
+        TileAt<TR> at;
+        const bool more = at.find(p, seg, __shfl_sync(0xffffffffu, ticket, 0), lane, reverse) && ends == 0;
+        if (n >= S && !wait(&blk.empty[n % S], n / S - 1)) break;
         TileInfo<TR> &info = blk.info[n % S];
         if (more) {
             if (lane == 0) {
@@ -586,21 +629,15 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(OPS * OP_BYTES)
                                  : "memory");
-                    load_tile(dst, m0, int(strip) * TC, int(row0), bar, once);
-                    load_tile(dst + OP_BYTES, m1, int(strip) * TC, int(row0), bar, once);
-                    if constexpr (OPS == 3) load_tile(dst + 2 * OP_BYTES, m2, int(strip) * TC, int(row0), bar, once);
+                    load_tile(dst, m0, at.strip * TC, int(at.row0), bar, once);
+                    load_tile(dst + OP_BYTES, m1, at.strip * TC, int(at.row0), bar, once);
+                    if constexpr (OPS == 3) load_tile(dst + 2 * OP_BYTES, m2, at.strip * TC, int(at.row0), bar, once);
                 }
                 ticket = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : uint32_t(p.n_strips);
-                info.row0 = row0;
-                info.row_end = row_end;
-                info.state_row = state;
-                info.strip = int(strip);
-                info.place = seg.c;
-                info.word = word;
-                info.last = seg.c + 1 == count;
+                at.put(info);
             }
             __syncwarp();
-            fill_info<TR>(p, bounds, row0, row_end, info, lane);
+            fill_info<TR>(p, bounds, at.row0, at.row_end, info, lane);
         } else {
             ++ends;
         }
@@ -608,6 +645,12 @@ __device__ __forceinline__ void feed(const GatedParams &p, B &blk, uint32_t slot
         __syncwarp();
         if (lane == 0) arrive(&blk.full[n % S]);
     }
+    if (lane == 0) {
+        blk.fed = n;
+        blk.ticket = ticket;
+    }
+    if (ends < kCarryWarps)
+        for (int m = n > S ? n - S : 0; m < n; ++m) mbar_wait(smem_addr(&blk.full[m % S]), uint32_t(m / S & 1), kCopyWait);
 }
 
 // Maps of a channel's E elements composed: `then` after `first`.
@@ -643,10 +686,10 @@ template <class V> __device__ __forceinline__ V apply_vec(V A, V B, V h) {
 template <int E, int S, int TR, int DIR, class B>
 __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, int lane) {
     using V = typename FVec<E>::type;
-    Waiter wait{p.status, kTileWait};
+    const Waiter wait{&blk.lost, p.tile_wait};
     workspace_ready();
     for (int n = c;; n += kCarryWarps) {
-        wait(&blk.full[n % S], n / S);
+        if (!wait(&blk.full[n % S], n / S)) return;
         const TileInfo<TR> &info = blk.info[n % S];
         if (!info.there) return;
         const int64_t strip = info.strip, state = info.state_row;
@@ -661,7 +704,7 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
         if constexpr (DIR < 0) {
             if (info.start[0] < 0 && !last) hf = state_row<E>(p.states, state * p.D, d0, p.D);
         }
-        wait(&blk.maps[e0], n / kQ);
+        if (!wait(&blk.maps[e0], n / kQ)) return;
         V A[kWarps], B_[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -708,6 +751,81 @@ __device__ __forceinline__ void carry_loop(const GatedParams &p, B &blk, int c, 
         } else {
             if (lane == 0) arrive(&blk.in[e0]);
         }
+    }
+}
+
+// What a lost block still does (all of it, its loops ended): NaN for the tiles
+// that not every data warp has replayed, whose tables are still in their
+// slots, then for the ticket in hand and all it can draw; and NaN handed on, so
+// that no other block waits for these tiles.
+template <typename IO, int E, int S, int TR, int DIR, class B>
+__device__ __noinline__ void give_up(const GatedParams &p, B &blk, int warp, int lane) {
+    using V = typename FVec<E>::type;
+    using W = typename Raw<IO, E>::type;
+    constexpr int R = TR / kWarps;
+    const V bad = vset<V>(nan_value());
+    const W out = Conv<IO, E>::out(bad);
+    auto spoil = [&](const TileInfo<TR> &info) {
+        const int64_t d0 = int64_t(info.strip) * 32 * E + lane * E;
+        if (warp < kWarps) {
+            const uint4 k = info.masks[warp];
+            for (int r = 0; r < R; ++r) {
+                const int64_t row = info.row0 + warp * R + r;
+                if (row >= info.row_end) break;
+                const bool live = k.z >> r & 1u;
+                if (d0 < p.D && (live || p.zero_padding)) {
+                    if constexpr (DIR > 0) {
+                        reinterpret_cast<W *>(static_cast<char *>(p.h) + (row * p.h_rs + d0) * int64_t(sizeof(IO)))[0] = live ? out : W(0);
+                    } else {
+                        reinterpret_cast<W *>(static_cast<char *>(p.df) + (row * p.df_rs + d0) * int64_t(sizeof(IO)))[0] = live ? out : W(0);
+                        reinterpret_cast<W *>(static_cast<char *>(p.dv) + (row * p.dv_rs + d0) * int64_t(sizeof(IO)))[0] = live ? out : W(0);
+                    }
+                }
+                if constexpr (DIR > 0) {
+                    if ((k.y >> r & 1u) && p.h_last) put_state_row<E>(p.h_last, info.end[warp * R + r] * p.D, d0, p.D, bad);
+                } else {
+                    if ((k.x >> r & 1u) && p.dh0) put_state_row<E>(p.dh0, info.start[warp * R + r] * p.D, d0, p.D, bad);
+                }
+            }
+        } else if (warp == kWarps) {
+            if (DIR > 0 && p.states) {
+                put_state_row<E>(p.states, info.state_row * p.D, d0, p.D, bad);
+                if (info.row0 + kBwdTR < info.row_end) put_state_row<E>(p.states, (info.state_row + 1) * p.D, d0, p.D, bad);
+            }
+            if (p.words && !info.last) {
+                const int64_t at = (info.word * p.n_strips + info.strip) * 32 * E + lane * E;
+                for (int e = 0; e < E; ++e) st_relaxed_u64(p.words + at + e, word_of(-0.f, nan_value()));
+            }
+        }
+    };
+    workspace_ready();
+    if (threadIdx.x == 0 && p.status) atomicExch(p.status, 5u);      // SGR_ERR_TIMEOUT
+    int from = blk.fed;
+    for (int w = 0; w < kWarps; ++w) from = blk.done[w] < from ? blk.done[w] : from;
+    for (int n = from; n < blk.fed; ++n)
+        if (blk.info[n % S].there) spoil(blk.info[n % S]);
+    const Bounds bounds{p, nullptr};
+    Segments<TR> seg;
+    seg.init(p, bounds, lane);
+    uint32_t ticket = blk.ticket;
+    for (;;) {
+        __syncthreads();
+        if (warp == kThreads / 32 - 1) {
+            TileAt<TR> at;
+            const bool more = at.find(p, seg, __shfl_sync(0xffffffffu, ticket, 0), lane, DIR < 0);
+            if (more) {
+                if (lane == 0) {
+                    ticket = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : uint32_t(p.n_strips);
+                    at.put(blk.info[0]);
+                }
+                __syncwarp();
+                fill_info<TR>(p, bounds, at.row0, at.row_end, blk.info[0], lane);
+            }
+            if (lane == 0) blk.info[0].there = more;
+        }
+        __syncthreads();
+        if (!blk.info[0].there) break;
+        spoil(blk.info[0]);
     }
 }
 
@@ -779,7 +897,7 @@ template <typename IO, int E, bool TMA> struct ForwardShape {
 
 template <typename IO, int E, int GATE, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
-gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_v) {
+gated_scan_kernel(const __grid_constant__ GatedParams p, const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_v) {
     using V = typename FVec<E>::type;
     using W = typename Raw<IO, E>::type;
     using C = Conv<IO, E>;
@@ -792,11 +910,12 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     init_block<S>(blk);
     if (warp < kWarps) {
-        Waiter wait{p.status, kTileWait};
+        const Waiter wait{&blk.lost, p.tile_wait};
         V gate[2][R];
         // tile n: gates into registers, the warp's map to shared memory; false behind the last tile
+        // and where a wait ran out
         auto fold = [&](int n, V (&g)[R]) {
-            const bool got = wait(&blk.full[n % S], n / S);
+            if (!wait(&blk.full[n % S], n / S)) return false;
             const TileInfo<kTR> &info = blk.info[n % S];
             if (!info.there) return false;
             const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
@@ -827,7 +946,6 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
                     A = vmul(A, a);
                 }
             }
-            if (!got) A = B = vset<V>(nan_value());
             blk.A[0][n % kQ][warp][lane] = A;
             blk.B[0][n % kQ][warp][lane] = B;
             __syncwarp();
@@ -842,8 +960,8 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
             const bool dvalid = d0 < p.D;
             char *dst = static_cast<char *>(p.h) + (row * p.h_rs + d0) * int64_t(sizeof(IO));
             const int64_t pitch = p.h_rs * int64_t(sizeof(IO));
-            const bool got = wait(&blk.in[n % kQ], n / kQ);
-            V h = got ? entering<0>(blk, n % kQ, warp, lane, blk.enter[n % kQ][lane]) : vset<V>(nan_value());
+            if (!wait(&blk.in[n % kQ], n / kQ)) return false;
+            V h = entering<0>(blk, n % kQ, warp, lane, blk.enter[n % kQ][lane]);
             if (k.w) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -870,23 +988,30 @@ gated_scan_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f
             }
             __syncwarp();
             if (lane == 0) arrive(&blk.empty[n % S]);
+            return true;
         };
         // one copy of either body: with two, for registers that need not move, the warps
         // spent a fifth of their time waiting for instructions
+        int done = 0;
 #pragma unroll 1
         for (int n = 0;; ++n) {
             const bool more = fold(n, gate[0]);
-            if (n > 0) replay(n - 1, gate[1]);
+            if (n > 0) {
+                if (!replay(n - 1, gate[1])) break;
+                done = n;
+            }
             if (!more) break;
 #pragma unroll
             for (int r = 0; r < R; ++r) gate[1][r] = gate[0][r];
         }
+        if (lane == 0) blk.done[warp] = done;
     } else if (warp < kWarps + kCarryWarps) {
         carry_loop<E, S, kTR, 1>(p, blk, warp - kWarps, lane);
     } else {
         feed<S, 2, kTR, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, false, &map_f, &map_v, nullptr);
     }
     __syncthreads();
+    if (blk.lost) give_up<IO, E, S, kTR, 1>(p, blk, warp, lane);
     empty_sequences(p, p.h_last, p.h0, p.h0_ss);
 }
 
@@ -937,7 +1062,7 @@ template <typename IO, int E, bool TMA> struct BackwardShape {
 
 template <typename IO, int E, int GATE, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
-gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensorMap map_f,
+gated_scan_backward_kernel(const __grid_constant__ GatedParams p, const __grid_constant__ CUtensorMap map_f,
                            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dh) {
     using V = typename FVec<E>::type;
     using W = typename Raw<IO, E>::type;
@@ -951,10 +1076,10 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     init_block<S>(blk);
     if (warp < kWarps) {
-        Waiter wait{p.status, kTileWait};
+        const Waiter wait{&blk.lost, p.tile_wait};
         V gate[2][R];
         auto fold = [&](int n, V (&s)[R]) {
-            const bool got = wait(&blk.full[n % S], n / S);
+            if (!wait(&blk.full[n % S], n / S)) return false;
             const TileInfo<kBwdTR> &info = blk.info[n % S];
             if (!info.there) return false;
             const int64_t row = info.row0 + warp * R, d0 = int64_t(info.strip) * TC + lane * E;
@@ -1007,7 +1132,6 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
                     RA = vmul(RA, a);
                 }
             }
-            if (!got) A = B = RA = RB = vset<V>(nan_value());
             blk.A[0][n % kQ][warp][lane] = RA;
             blk.B[0][n % kQ][warp][lane] = RB;
             blk.A[1][n % kQ][warp][lane] = A;
@@ -1023,7 +1147,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             const auto dh = reader<IO, E, TMA, R, Shape, 2>(p, smem, n % S, warp, lane, row, d0, p.dh, p.dh_rs);
             const uint4 k = info.masks[warp];
             const bool dvalid = d0 < p.D;
-            const bool got = wait(&blk.in[n % kQ], n / kQ);
+            if (!wait(&blk.in[n % kQ], n / kQ)) return false;
             V h = blk.A[1][n % kQ][warp][lane];
             V c[R];                                                   // df = c g
             auto forward = [&](auto plain) {
@@ -1045,7 +1169,7 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             };
             if (k.w) forward(std::true_type{});
             else forward(std::false_type{});
-            V flow = got ? entering<kWarps - 1>(blk, n % kQ, warp, lane, blk.enter[n % kQ][lane]) : vset<V>(nan_value());
+            V flow = entering<kWarps - 1>(blk, n % kQ, warp, lane, blk.enter[n % kQ][lane]);
             char *pf = static_cast<char *>(p.df) + ((row + R - 1) * p.df_rs + d0) * int64_t(sizeof(IO));
             char *pv = static_cast<char *>(p.dv) + ((row + R - 1) * p.dv_rs + d0) * int64_t(sizeof(IO));
             const int64_t pitch_f = p.df_rs * int64_t(sizeof(IO)), pitch_v = p.dv_rs * int64_t(sizeof(IO));
@@ -1083,23 +1207,30 @@ gated_scan_backward_kernel(const GatedParams p, const __grid_constant__ CUtensor
             }
             __syncwarp();
             if (lane == 0) arrive(&blk.empty[n % S]);
+            return true;
         };
         // one copy of either body: with two, for registers that need not move, the warps
         // spent a fifth of their time waiting for instructions
+        int done = 0;
 #pragma unroll 1
         for (int n = 0;; ++n) {
             const bool more = fold(n, gate[0]);
-            if (n > 0) replay(n - 1, gate[1]);
+            if (n > 0) {
+                if (!replay(n - 1, gate[1])) break;
+                done = n;
+            }
             if (!more) break;
 #pragma unroll
             for (int r = 0; r < R; ++r) gate[1][r] = gate[0][r];
         }
+        if (lane == 0) blk.done[warp] = done;
     } else if (warp < kWarps + kCarryWarps) {
         carry_loop<E, S, kBwdTR, -1>(p, blk, warp - kWarps, lane);
     } else {
         feed<S, 3, kBwdTR, Shape::op_bytes, TC, TMA>(p, blk, smem_addr(smem), lane, true, &map_f, &map_v, &map_dh);
     }
     __syncthreads();
+    if (blk.lost) give_up<IO, E, S, kBwdTR, -1>(p, blk, warp, lane);
     empty_sequences(p, p.dh0, p.dh_last, p.D);
 }
 

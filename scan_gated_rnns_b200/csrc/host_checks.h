@@ -115,8 +115,9 @@ inline cudaError_t allow_smem(int bytes) {
 }
 
 // The testing hooks of the chunk hand-off (sgr_set_wait_limit,
-// sgr_set_drop_publish), as they are set now.
+// sgr_set_block_wait_limit, sgr_set_drop_publish), as they are set now.
 uint32_t wait_limit();
+uint32_t block_wait_limit();
 int64_t drop_tile();
 
 inline int float_size(sgr_dtype_t t) { return t == SGR_F32 ? 4 : (t == SGR_BF16 || t == SGR_F16 ? 2 : 0); }

@@ -118,6 +118,7 @@ std::atomic<int> g_override_kind{KIND_AUTO};
 // graphs, which zero the words inside the graph first.
 std::atomic<uint64_t> g_epoch{2};
 std::atomic<uint32_t> g_spin_limit{sgr::kSpinLimit};
+std::atomic<uint32_t> g_block_wait_limit{0};
 std::atomic<int64_t> g_drop_tile{-1};
 
 uint32_t next_epoch() {
@@ -1589,6 +1590,7 @@ sgr_status_t run_projected_scan(const void *x, const void *w, const float *h0, i
 }  // namespace
 
 uint32_t sgr::host::wait_limit() { return g_spin_limit.load(); }
+uint32_t sgr::host::block_wait_limit() { return g_block_wait_limit.load(); }
 int64_t sgr::host::drop_tile() { return g_drop_tile.load(); }
 
 extern "C" {
@@ -1914,6 +1916,11 @@ int sgr_backward_kernel(sgr_op_t op, int64_t B, int64_t T, int64_t D, sgr_dtype_
 
 sgr_status_t sgr_set_wait_limit(uint32_t polls) {
     g_spin_limit.store(polls == 0 ? sgr::kSpinLimit : polls);
+    return SGR_OK;
+}
+
+sgr_status_t sgr_set_block_wait_limit(uint32_t polls) {
+    g_block_wait_limit.store(polls);
     return SGR_OK;
 }
 

@@ -171,6 +171,7 @@ def hooks():
     lib = _abi.lib()
     yield lib
     lib.sgr_set_wait_limit(0)
+    lib.sgr_set_block_wait_limit(0)
     lib.sgr_set_drop_publish(-1)
 
 
@@ -232,3 +233,50 @@ def test_workspaces_that_do_not_fit():
     with pytest.raises(ValueError, match="workspace"):
         sgr.gated_scan(f, f, workspace=sgr.Workspace(need, "cpu"))
     assert torch.equal(sgr.gated_scan(f[:50], f[:50], workspace=sgr.Workspace(16, DEV))[0], f[:50])   # needs none
+
+
+def right_or_nan(got, want):
+    """Every value has the clean call's bits or is NaN; whether one is NaN."""
+    odd = got != want
+    assert bool(got[odd].isnan().all())
+    return bool(odd.any())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,D,n,layout", [(30000, 320, 7, "plain"), (9000, 160, 40, "odd"), (60, 64, 3, "plain"),
+                                             (180, 33, 1, "odd"), (40000, 64, 1, "plain")])
+def test_blocks_that_give_up(rows, D, n, layout, dtype, hooks):
+    """Waits between a block's warps so short that some run out: every value is
+    right or NaN, what lies beside the sequences stays, and the call says so."""
+    rng = np.random.default_rng(rows)
+    (f, v, dh, h0, dl), _ = operands(dtype, rng.normal(size=(rows, D)), 3, n)
+    if layout == "odd":
+        f, v, dh = (torch.cat([x[:, :1], x], 1)[:, 1:] for x in (f, v, dh))
+    cu = torch.tensor([2, *sorted(rng.integers(2, rows - 5, n - 1).tolist()), rows - 5], device=DEV)
+    ws = sgr.Workspace(max(16, sgr.workspace_size("gated", 1, rows, D, dtype)), DEV)
+
+    def forward():
+        out = torch.full((rows, D), 7.0, dtype=dtype, device=DEV)
+        return sgr.gated_scan(f, v, h0, cu, out=out, save_states=True, workspace=ws)
+
+    def backward():
+        return sgr.gated_scan_backward(f, v, h0, states, dh, dl, cu, workspace=ws)
+
+    *clean, states = forward()
+    back = backward()
+    assert ws.status() == 0
+    lost = 0
+    for polls in (1, 1, 1, 2, 3):
+        hooks.sgr_set_block_wait_limit(polls)
+        for call, want in ((forward, clean), (backward, back)):
+            got = call()
+            said = ws.status()
+            bad = [right_or_nan(a, b) for a, b in zip(got, want)]
+            lost += any(bad)
+            assert said == _abi.SGR_ERR_TIMEOUT or not any(bad) or rows <= 192
+            assert bool((got[0][:2] == want[0][:2]).all()) and bool((got[0][rows - 5:] == want[0][rows - 5:]).all())
+        hooks.sgr_set_block_wait_limit(0)
+        for a, b in zip([*forward()[:2], *backward()], [*clean, *back]):
+            assert torch.equal(a, b)
+        assert ws.status() == 0
+    assert lost or rows < 30000
