@@ -579,7 +579,9 @@ SGR_API int sgr_backward_kernel(sgr_op_t op, int64_t B, int64_t T, int64_t D, sg
  *   gradient's waits between the warps of a block (0: twice the number of the
  *   other hook).  One that runs out makes its block give up: what that block
  *   had not finished, and the chunks it draws from then on, become NaN, and the
- *   workspace's first word SGR_ERR_TIMEOUT.
+ *   workspace's first word SGR_ERR_TIMEOUT.  Also of int8_projection's wait for a
+ *   tile's sums when it multiplies many tokens (0: 2^16); rows behind one that
+ *   runs out become NaN.
  * sgr_set_drop_publish: the block with this tile index (chunk * n_chains +
  *   chain) skips publishing its state, so the chunk after it in the same
  *   channels waits until the limit, records SGR_ERR_TIMEOUT in the workspace
@@ -696,7 +698,9 @@ SGR_API sgr_status_t int8_quantize(const void *x, int64_t x_row_stride, int8_t *
  *   w       : (N, K) signed 8-bit, w_scale fp32 (N), bias fp32 (N) or NULL.
  *   y       : (rows, N) of y_dtype (SGR_F32, SGR_BF16 or SGR_F16).
  * Strides are in elements.  w (and 8-bit x) whose rows start on 16-byte
- * boundaries take the tensor-core kernel, others a slower one.
+ * boundaries take the tensor-core kernel, others a slower one.  The kernels'
+ * waits are bounded (a fraction of a second each); outputs behind one that runs
+ * out are NaN.
  *   workspace: sgr_int8_workspace_size(rows, K, x_dtype) bytes, uninitialised.
  */
 SGR_API sgr_status_t int8_projection(const void *x, int64_t x_row_stride, sgr_dtype_t x_dtype, const float *x_scale,

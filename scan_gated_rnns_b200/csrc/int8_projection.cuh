@@ -22,6 +22,7 @@ struct ProjectParams {
     void *y;
     int64_t y_rs;                  // elements
     int64_t M, N, K;
+    uint32_t epilogue_wait;        // polls, of about 4 us, of the pair kernel's epilogue for a product
 };
 
 template <typename OUT>

@@ -17,7 +17,7 @@ namespace sgr {
 namespace i8 {
 
 constexpr int kKB = 128;                       // K bytes per stage
-constexpr uint32_t kWait = 1u << 16;        // polls of a wait (each suspends for tens of us)
+constexpr uint32_t kWait = 1u << 16;           // polls of a wait (each suspends for about 4 us)
 
 // kind::i8 instruction descriptor: s8 x s8 -> s32, both K-major
 constexpr uint32_t idesc(int m, int n) {
@@ -322,7 +322,9 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
 // tokens.  Against a tile of 128 x 256 per SM this needs two thirds of the
 // bytes from L2 for the same product, which is what bounds an 8-bit product
 // of this size first.  Two accumulators: the epilogue of a tile runs under
-// the next one's product.  Measured: 8192 x 4096 x 8192 to bf16 198 us, 2.8
+// the next one's product.  A warp of the epilogue whose wait runs out writes
+// NaN from there on and hands no accumulator back, so that the products stop
+// and the other warps' waits run out in turn.  Measured: 8192 x 4096 x 8192 to bf16 198 us, 2.8
 // POP/s, 0.85 of twice the bf16 rate of a large library product; the tensor
 // cores' rate under the power limit bounds it.
 namespace pair {
@@ -458,7 +460,7 @@ int8_project_pair_kernel(const ProjectParams p, int n_channel_tiles, int n_tiles
                 const int64_t m = tok0 + lane + 32 * i;
                 s_sx[lane + 32 * i] = m < p.M ? p.x_scale[m] : 0.f;
             }
-            if (!lost && !mbar_wait(acc_full(a), uint32_t((it / 2) & 1), kWait)) lost = true;
+            if (!lost && !mbar_wait(acc_full(a), uint32_t((it / 2) & 1), p.epilogue_wait)) lost = true;
             lost = __any_sync(0xffffffffu, lost);
             asm volatile("tcgen05.fence::after_thread_sync;");
             const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(a * kTok + half * 128);
@@ -467,7 +469,9 @@ int8_project_pair_kernel(const ProjectParams p, int n_channel_tiles, int n_tiles
                 uint32_t r[32];
                 tmem_ld32(taddr + t0, r);
                 tmem_wait();
-                if (t0 == 96) {                                    // the accumulator has been read
+                // the accumulator has been read; a warp that gave up never says so, or its
+                // arrivals would hand accumulators on that others still read
+                if (t0 == 96 && !lost) {
                     asm volatile("tcgen05.fence::before_thread_sync;");
                     __syncwarp();
                     if (lane == 0)

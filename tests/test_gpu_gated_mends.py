@@ -280,3 +280,22 @@ def test_blocks_that_give_up(rows, D, n, layout, dtype, hooks):
             assert torch.equal(a, b)
         assert ws.status() == 0
     assert lost or rows < 30000
+
+
+@pytest.mark.parametrize("K", [300, 12000])
+def test_projection_whose_epilogue_gives_up(K, hooks):
+    """Many tokens, several tiles a pair of SMs: warps that give up waiting for
+    their sums must not hand accumulators on that others still read.  A poll
+    takes some 4 us, a tile of the longer rows 40."""
+    M, N = 5000, 4096
+    x = torch.randint(-127, 128, (M, -(-K // 16) * 16), dtype=torch.int8, device=DEV)[:, :K]
+    w = torch.randint(-127, 128, (N, -(-K // 16) * 16), dtype=torch.int8, device=DEV)[:, :K]
+    sx, sw = torch.rand(M, device=DEV) + 0.5, torch.rand(N, device=DEV) + 0.5
+    want = sgr.int8_projection(x, w, sw, x_scale=sx)
+    lost = 0
+    for polls in (1, 2, 3):
+        hooks.sgr_set_block_wait_limit(polls)
+        lost += right_or_nan(sgr.int8_projection(x, w, sw, x_scale=sx), want)
+        hooks.sgr_set_block_wait_limit(0)
+        assert torch.equal(sgr.int8_projection(x, w, sw, x_scale=sx), want)
+    assert lost or K < 12000
