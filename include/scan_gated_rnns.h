@@ -580,8 +580,8 @@ SGR_API int sgr_backward_kernel(sgr_op_t op, int64_t B, int64_t T, int64_t D, sg
  *   other hook).  One that runs out makes its block give up: what that block
  *   had not finished, and the chunks it draws from then on, become NaN, and the
  *   workspace's first word SGR_ERR_TIMEOUT.  Also of int8_projection's wait for a
- *   tile's sums when it multiplies many tokens (0: 2^16); rows behind one that
- *   runs out become NaN.
+ *   tile's sums when it multiplies many tokens (0: half a second); rows behind
+ *   one that runs out become NaN.
  * sgr_set_drop_publish: the block with this tile index (chunk * n_chains +
  *   chain) skips publishing its state, so the chunk after it in the same
  *   channels waits until the limit, records SGR_ERR_TIMEOUT in the workspace

@@ -195,7 +195,9 @@ sgr_status_t int8_projection(const void *x, int64_t x_row_stride, sgr_dtype_t x_
     p.x = static_cast<const int8_t *>(x); p.x_rs = x_row_stride; p.x_scale = x_scale;
     p.w = w; p.w_rs = w_row_stride; p.w_scale = w_scale; p.bias = bias;
     p.y = y; p.y_rs = y_row_stride; p.M = rows; p.N = N; p.K = K;
-    p.epilogue_wait = host::block_wait_limit() ? host::block_wait_limit() : kWait;
+    const uint32_t hook = host::block_wait_limit();
+    p.epilogue_polls = hook ? hook : kPolls;
+    p.epilogue_ns = hook ? 0 : kWaitNs;
     if (x_dtype != SGR_I8) {
         int8_t *q = static_cast<int8_t *>(workspace);
         float *scale = reinterpret_cast<float *>(static_cast<char *>(workspace) + scale_at(rows, K));

@@ -22,7 +22,8 @@ struct ProjectParams {
     void *y;
     int64_t y_rs;                  // elements
     int64_t M, N, K;
-    uint32_t epilogue_wait;        // polls, of about 4 us, of the pair kernel's epilogue for a product
+    uint32_t epilogue_polls;       // polls of the pair kernel's epilogue for a product,
+    uint64_t epilogue_ns;          // and how long it goes on behind them
 };
 
 template <typename OUT>

@@ -17,7 +17,29 @@ namespace sgr {
 namespace i8 {
 
 constexpr int kKB = 128;                       // K bytes per stage
-constexpr uint32_t kWait = 1u << 16;           // polls of a wait (each suspends for about 4 us)
+// Bounded waits.  A poll of an mbarrier suspends a whole warp for 4 us, but
+// returns after 75 ns where only some of its lanes poll, as they do here: a
+// wait polls kPolls times and then goes on by the clock.
+constexpr uint32_t kPolls = 1u << 10;
+constexpr uint64_t kWaitNs = 500000000;
+__device__ __forceinline__ uint64_t timer_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t phase, uint32_t polls = kPolls, uint64_t ns = kWaitNs) {
+    if (mbar_wait(bar, phase, polls)) return true;
+    const uint64_t t0 = timer_ns();
+    for (uint32_t i = 0; i < 1u << 28 && timer_ns() - t0 < ns; ++i)
+        if (mbar_try_wait(bar, phase)) return true;
+    return false;
+}
+// the copies still in flight at the end: at once, if `ok`; else they were
+// started a wait's length ago at least
+__device__ __forceinline__ void wait_at_end(uint32_t bar, uint32_t phase, bool ok) {
+    if (ok) wait_for(bar, phase);
+    else mbar_wait(bar, phase, kPolls);
+}
 
 // kind::i8 instruction descriptor: s8 x s8 -> s32, both K-major
 constexpr uint32_t idesc(int m, int n) {
@@ -181,12 +203,14 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
             tma_load_2d(ring + uint32_t(g) * S::stage_bytes, &map_w, (kb0 + g) * kKB, ct * 128, full(g));
         }
         grid_dependency_wait();
+        bool ok = true;
         for (int i = 0; i < g; ++i)
             tma_load_2d(ring + uint32_t(i) * S::stage_bytes + S::a_bytes, &map_x, (kb0 + i) * kKB, tt * NT, full(i));
         for (int kb = kb0 + g; kb < kb1; ++kb, ++g) {
             const int s = g % S::stages;
-            if (!mbar_wait(empty(s), uint32_t((g / S::stages - 1) & 1), kWait)) {
+            if (!wait_for(empty(s), uint32_t((g / S::stages - 1) & 1))) {
                 *s_bad = 1;
+                ok = false;
                 break;
             }
             const uint32_t dst = ring + uint32_t(s) * S::stage_bytes;
@@ -196,12 +220,13 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
         }
         // never leave with copies in flight
         for (int k = g > S::stages ? g - S::stages : 0; k < g; ++k)
-            mbar_wait(full(k % S::stages), uint32_t((k / S::stages) & 1), kWait);
+            wait_at_end(full(k % S::stages), uint32_t((k / S::stages) & 1), ok);
     } else if (warp == 1 && lane == 0) {
         int g = 0;
+        grid_dependency_wait();                                    // no wait's time passes while tokens are quantised
         for (int kb = kb0; kb < kb1; ++kb, ++g) {
             const int s = g % S::stages;
-            if (!mbar_wait(full(s), uint32_t((g / S::stages) & 1), kWait)) {
+            if (!wait_for(full(s), uint32_t((g / S::stages) & 1))) {
                 *s_bad = 1;
                 break;
             }
@@ -218,8 +243,8 @@ __global__ void __launch_bounds__(128, 2) int8_project_split_kernel(const Projec
                      ::"r"(done) : "memory");
     }
     __syncwarp();
-    if (!mbar_wait(done, 0, kWait)) *s_bad = 1;
-    grid_dependency_wait();                                        // the tokens' scales
+    grid_dependency_wait();                                        // the tokens and their scales
+    if (!wait_for(done, 0)) *s_bad = 1;
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;");
 
@@ -397,7 +422,7 @@ int8_project_pair_kernel(const ProjectParams p, int n_channel_tiles, int n_tiles
                 const int wy = ct * kCh + int(rank) * 128, xy = tt * kTok + int(rank) * 128;
                 for (int kb = 0; kb < n_kb; ++kb, ++g) {
                     const int s = int(g % kStages);
-                    if (g >= kStages && !mbar_wait(empty(s), uint32_t((g / kStages - 1) & 1), kWait)) {
+                    if (g >= kStages && !wait_for(empty(s), uint32_t((g / kStages - 1) & 1))) {
                         ok = false;
                         break;
                     }
@@ -410,7 +435,7 @@ int8_project_pair_kernel(const ProjectParams p, int n_channel_tiles, int n_tiles
             }
             // never leave with copies in flight: the last stages have been read once they are empty again
             for (int64_t k = g > kStages ? g - kStages : 0; k < g; ++k)
-                mbar_wait(empty(int(k % kStages)), uint32_t((k / kStages) & 1), kWait);
+                wait_at_end(empty(int(k % kStages)), uint32_t((k / kStages) & 1), ok);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -420,11 +445,11 @@ int8_project_pair_kernel(const ProjectParams p, int n_channel_tiles, int n_tiles
             bool ok = true;
             for (int tile = first; tile < n_tiles && ok; tile += pairs, ++n) {
                 const int a = n & 1;
-                if (n >= 2 && !mbar_wait(acc_empty(a), uint32_t((n / 2 - 1) & 1), kWait)) break;
+                if (n >= 2 && !wait_for(acc_empty(a), uint32_t((n / 2 - 1) & 1))) break;
                 asm volatile("tcgen05.fence::after_thread_sync;");
                 for (int kb = 0; kb < n_kb; ++kb, ++g) {
                     const int s = int(g % kStages);
-                    if (!mbar_wait(full(s), uint32_t((g / kStages) & 1), kWait)) {
+                    if (!wait_for(full(s), uint32_t((g / kStages) & 1))) {
                         ok = false;
                         break;
                     }
@@ -460,7 +485,7 @@ int8_project_pair_kernel(const ProjectParams p, int n_channel_tiles, int n_tiles
                 const int64_t m = tok0 + lane + 32 * i;
                 s_sx[lane + 32 * i] = m < p.M ? p.x_scale[m] : 0.f;
             }
-            if (!lost && !mbar_wait(acc_full(a), uint32_t((it / 2) & 1), p.epilogue_wait)) lost = true;
+            if (!lost && !wait_for(acc_full(a), uint32_t((it / 2) & 1), p.epilogue_polls, p.epilogue_ns)) lost = true;
             lost = __any_sync(0xffffffffu, lost);
             asm volatile("tcgen05.fence::after_thread_sync;");
             const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(a * kTok + half * 128);

@@ -299,3 +299,13 @@ def test_projection_whose_epilogue_gives_up(K, hooks):
         hooks.sgr_set_block_wait_limit(0)
         assert torch.equal(sgr.int8_projection(x, w, sw, x_scale=sx), want)
     assert lost or K < 12000
+
+
+def test_many_tokens_of_few_channels_quantised_within():
+    """The product is set up while a million rows are quantised and waits for
+    them: the same bits as in two calls."""
+    x = torch.randn(1 << 20, 256, device=DEV, dtype=BF16)
+    wq, ws = sgr.int8_quantize(torch.randn(96, 256, device=DEV))
+    y = sgr.int8_projection(x, wq, ws)
+    q, s = sgr.int8_quantize(x)
+    assert torch.equal(y, sgr.int8_projection(q, wq, ws, x_scale=s, out_dtype=BF16))
