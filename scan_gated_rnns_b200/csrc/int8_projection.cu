@@ -135,8 +135,9 @@ sgr_status_t product(const ProjectParams &p, sgr_dtype_t out, bool behind, cudaS
                                                 : launch_tensor<__half>(p, sms, behind, s);
         return e == cudaSuccess ? SGR_OK : SGR_ERR_CUDA;
     }
-    if ((p.M + 63) / 64 > 65535) return SGR_ERR_UNSUPPORTED;      // grid rows
-    const dim3 grid(unsigned((p.N + 63) / 64), unsigned((p.M + 63) / 64));
+    const int64_t tiles = ((p.N + 63) / 64) * ((p.M + 63) / 64);
+    if (tiles > std::numeric_limits<int>::max()) return SGR_ERR_UNSUPPORTED;
+    const dim3 grid{unsigned(tiles)};
     if (out == SGR_F32) int8_project_any_kernel<float><<<grid, 256, 0, s>>>(p);
     else if (out == SGR_BF16) int8_project_any_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
     else int8_project_any_kernel<__half><<<grid, 256, 0, s>>>(p);

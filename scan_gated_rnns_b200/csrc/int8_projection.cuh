@@ -232,7 +232,8 @@ __device__ __forceinline__ int load_word(const int8_t *row, int64_t k, int64_t K
 template <typename OUT>
 __global__ void __launch_bounds__(256) int8_project_any_kernel(const ProjectParams p) {
     __shared__ int s_x[64][17], s_w[64][17];
-    const int64_t m0 = int64_t(blockIdx.y) * 64, n0 = int64_t(blockIdx.x) * 64;
+    const unsigned across = unsigned((p.N + 63) / 64);
+    const int64_t m0 = int64_t(blockIdx.x / across) * 64, n0 = int64_t(blockIdx.x % across) * 64;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     int acc[4][4] = {};
     for (int64_t k0 = 0; k0 < p.K; k0 += 64) {

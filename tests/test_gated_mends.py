@@ -7,6 +7,8 @@ import torch
 
 from scan_gated_rnns_b200 import _abi, gated, ops
 
+from test_abi import fake_addresses
+
 
 @pytest.fixture
 def launches(monkeypatch):
@@ -38,3 +40,18 @@ def test_results_of_a_sliding_window_have_dense_rows(launches, shape):
     h, _ = gated.gated_scan_fn(f.requires_grad_(True), v)
     assert row_dense(h)
     assert [name for name, _ in launches] == ["gated_scan", "gated_scan_backward", "gated_step", "gated_scan"]
+
+
+# -------------------------------------------------------------- sizes
+def project(rows, K, N, x_rs, w_rs):
+    return _abi.lib().int8_projection(1 << 40, x_rs, _abi.SGR_I8, 2 << 40, 3 << 40, w_rs, 4 << 40, None, 5 << 40, N,
+                                      _abi.SGR_F32, rows, K, N, None, 0, None)
+
+
+@fake_addresses
+def test_projection_of_many_rows_at_any_alignment():
+    """Rows of 100 bytes: nothing refuses their number (no device is here, so
+    the launch is what fails)."""
+    for rows in (64 * 65535, 64 * 65535 + 1, 10 ** 7):
+        assert project(rows, 100, 8, 100, 100) == _abi.SGR_ERR_CUDA
+    assert project(1 << 30, 100, 1 << 14, 100, 100) == _abi.SGR_ERR_UNSUPPORTED      # tiles past 2^31 - 1

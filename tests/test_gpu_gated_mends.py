@@ -309,3 +309,13 @@ def test_many_tokens_of_few_channels_quantised_within():
     y = sgr.int8_projection(x, wq, ws)
     q, s = sgr.int8_quantize(x)
     assert torch.equal(y, sgr.int8_projection(q, wq, ws, x_scale=s, out_dtype=BF16))
+
+
+def test_projection_of_many_rows_at_any_alignment():
+    """More tiles of 64 rows than a grid has rows, on rows of an odd length."""
+    M, K, N = 64 * 65536 + 1, 3, 2
+    x = torch.randint(-127, 128, (M, K), dtype=torch.int8, device=DEV)
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device=DEV)
+    one = torch.ones(M, device=DEV)
+    y = sgr.int8_projection(x, w, one[:N], x_scale=one)
+    assert torch.equal(y, (x.int()[:, None, :] * w.int()[None]).sum(-1).float())
