@@ -153,7 +153,8 @@ sgr_status_t run(GatedParams &p, sgr_dtype_t dtype, sgr_gate_t gate, bool backwa
         return SGR_ERR_INVALID_ARG;
     if (p.D == 0 || (p.rows == 0 && p.n_seqs == 0)) return SGR_OK;
     if (p.f_rs < 0 || p.v_rs < 0 || p.h_rs < 0 || p.dh_rs < 0 || p.df_rs < 0 || p.dv_rs < 0) return SGR_ERR_INVALID_ARG;
-    if (!sizes_ok(p.rows, p.D) || p.n_seqs > std::numeric_limits<int>::max()) return SGR_ERR_UNSUPPORTED;
+    // the search for bounds adds up to 32 to their number, in 32 bits
+    if (!sizes_ok(p.rows, p.D) || p.n_seqs > std::numeric_limits<int>::max() - 63) return SGR_ERR_UNSUPPORTED;
     const int tr = backward ? kBwdTR : kTR;
     const int64_t n_chunks = (p.rows + tr - 1) / tr, n_states = sgr_gated_chunks(p.rows);
     if (p.rows > 0) {

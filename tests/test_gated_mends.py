@@ -55,3 +55,14 @@ def test_projection_of_many_rows_at_any_alignment():
     for rows in (64 * 65535, 64 * 65535 + 1, 10 ** 7):
         assert project(rows, 100, 8, 100, 100) == _abi.SGR_ERR_CUDA
     assert project(1 << 30, 100, 1 << 14, 100, 100) == _abi.SGR_ERR_UNSUPPORTED      # tiles past 2^31 - 1
+
+
+@fake_addresses
+def test_scan_of_the_most_sequences():
+    """The bounds' search counts sequences in 32 bits, 32 at a time."""
+    def scan(n):
+        return _abi.lib().gated_scan(1 << 40, 8, 2 << 40, 8, None, 0, 3 << 40, 4, n, 4 << 40, 8, None, None, 400, 8,
+                                     _abi.SGR_GATE_LOG, _abi.SGR_F32, 1, 5 << 40, 1 << 30, None)
+
+    assert scan(2 ** 31 - 1) == _abi.SGR_ERR_UNSUPPORTED and scan(2 ** 31 - 32) == _abi.SGR_ERR_UNSUPPORTED
+    assert scan(2 ** 31 - 64) == _abi.SGR_ERR_CUDA
