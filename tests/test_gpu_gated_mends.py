@@ -319,3 +319,16 @@ def test_projection_of_many_rows_at_any_alignment():
     one = torch.ones(M, device=DEV)
     y = sgr.int8_projection(x, w, one[:N], x_scale=one)
     assert torch.equal(y, (x.int()[:, None, :] * w.int()[None]).sum(-1).float())
+
+
+@pytest.mark.parametrize("step", [16, 48, 128, 8])
+@pytest.mark.parametrize("rows", [5, 300, 3000])
+def test_projection_of_a_sliding_window(rows, step):
+    """8-bit rows that overlap one another, as tokens and as channels."""
+    K, N = 128, 600
+    g = torch.Generator(device=DEV).manual_seed(rows + step)
+    x = torch.randint(-127, 128, (step * rows + K,), dtype=torch.int8, device=DEV, generator=g).unfold(0, K, step)[:rows]
+    w = torch.randint(-127, 128, (step * N + K,), dtype=torch.int8, device=DEV, generator=g).unfold(0, K, step)[:N]
+    one = torch.ones(max(rows, N), device=DEV)
+    y = sgr.int8_projection(x, w, one[:N], x_scale=one[:rows])
+    assert torch.equal(y, (x.double() @ w.double().t()).float())
