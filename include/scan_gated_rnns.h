@@ -625,8 +625,12 @@ SGR_API sgr_status_t sgr_set_drop_publish(int64_t tile);
  *                initialised and keeps nothing from call to call.  Not to be
  *                shared with another call that can run at the same time, nor
  *                with the entry points that keep hand-off words in theirs.
- * States and arithmetic are fp32.  A NaN or infinity stays within its sequence
- * and channel (behind an infinite state the sequence holds infinities or NaN).  The result does not depend on how blocks are timed: equal
+ * No output may share bytes, from its first element to its last, with an input
+ * or another output.
+ * States and arithmetic are fp32; every type's gates keep the smaller of a and
+ * 1 - a, and decays next to 1, to fp32's own precision.  A NaN or infinity stays
+ * within its sequence and channel (behind an infinite state the sequence holds
+ * infinities or NaN).  The result does not depend on how blocks are timed: equal
  * calls give equal bits.  Calls may be captured.  A chunk that waited too long
  * for an earlier one (sgr_set_wait_limit) leaves NaN in the rest of its channels'
  * segment and sets the workspace's first word to SGR_ERR_TIMEOUT; a call that
@@ -642,7 +646,8 @@ SGR_API sgr_status_t gated_scan(const void *f, int64_t f_row_stride, const void 
  * gated_scan_backward -- gradients through gated_scan.  With g_t = dh_t +
  * a_{t+1} g_{t+1} within a sequence (its last row adds dh_last):
  *     SGR_GATE_SIGMOID: dv = (1 - a) g,  df = a (1 - a) (h_{t-1} - v) g
- *     SGR_GATE_LOG:     dv = g,          df = [f <= 0] a h_{t-1} g
+ *     SGR_GATE_LOG:     dv = g,          df = [f <= 0] a h_{t-1} g (0 where f > 0,
+ *                       whatever h and g are)
  *   states  : as gated_scan left them for the same f, v, h0 and bounds.
  *   dh      : (rows, D) in dtype; dh_last: fp32 (n_seqs, D) or NULL (0).
  *   df, dv  : (rows, D) in dtype; 0 at padding rows.
@@ -670,7 +675,8 @@ SGR_API int64_t sgr_gated_chunks(int64_t rows);
  *   slots : `rows` slot numbers on the device, slot_bytes 4 or 8 each; NULL:
  *           row i has slot i.  Rows whose slot is negative or at least n_slots
  *           are padding: h is 0 there if zero_padding, else left as it was.  A
- *           slot that several rows name takes their tokens in row order.
+ *           slot that several rows name takes their tokens in row order.  Each
+ *           row looks through all of them: meant for some thousand rows at most.
  *   h     : (rows, D) in dtype; must not overlap f, v or state.
  */
 SGR_API sgr_status_t gated_step(const void *f, int64_t f_row_stride, const void *v, int64_t v_row_stride, float *state,

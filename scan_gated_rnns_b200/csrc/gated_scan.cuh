@@ -44,12 +44,15 @@
 //
 // Measured (B200, SM clock 1965 MHz; bytes = f, v in and h out, or f, v, dh in
 // and df, dv out, over the 6549 GB/s of a copy): forward fp32 131072 x 512
-// 154 us (0.80), fp32 8 x 4096 x 1024 79 us (0.78), bf16 32768 x 4096 in 23
-// sequences 165 us (0.74); backward fp32 8 x 4096 x 1024 125 us (0.82), bf16
-// 16384 x 2048 85 us (0.60).  Bound by: the wait for the carried state where
-// one long sequence keeps the segments at one; memory at about 5.6 TB/s and
-// some 10 us of start and end otherwise; instruction issue (49 % busy) in the
-// 16-bit gradient.
+// 155 us (0.79), fp32 8 x 4096 x 1024 77 us (0.80), bf16 32768 x 4096 in 23
+// sequences 186 us (0.66; log gate 166, 0.74); backward fp32 8 x 4096 x 1024
+// 125 us (0.82), bf16 16384 x 2048 98 us (0.52; log gate 88).  Bound by: the
+// wait for the carried state where one long sequence keeps the segments at
+// one; memory at about 5.6 TB/s and some 10 us of start and end in fp32; in
+// 16 bits by too little independent work for 15 warps: schedulers issue in 40
+// (forward) and 48 % (backward) of the cycles, and a warp spends 37 and 27 % of
+// its time behind barriers and loads, 12 and 17 % behind fixed latencies, 10
+// and 7 % behind instruction fetch.
 #pragma once
 
 #include "gated_math.cuh"

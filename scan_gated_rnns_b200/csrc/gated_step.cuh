@@ -61,7 +61,10 @@ __device__ __forceinline__ void store_values(void *base, int64_t off, const Valu
 // named by an earlier row are taken by that row's block, in row order: a slot
 // that appears twice receives two tokens one after the other, and no two
 // blocks ever touch the same state.  The row's operands are on their way while
-// the slots are looked through; U vectors a thread keep enough bytes in flight
+// the slots are looked through, by every block the whole list: nothing beside
+// the rest up to some thousand rows, then quadratic (1024 bf16 channels: 4096
+// rows 25 us against 12 without slots, 32768 rows 890 against 91).  U vectors a
+// thread keep enough bytes in flight
 // (509 rows of 4096 bf16 channels, states in fp32: 9.2 us, 10.6 with one; their
 // 29 MB take 4.5 us from memory, the rest is the start and the slots' search).
 template <typename IO, int GATE, int V, int U>

@@ -287,7 +287,8 @@ def gated_step(f: torch.Tensor, v: torch.Tensor, state: torch.Tensor, slots: Opt
     slots: (M,) int32 or int64 on the GPU, the pool row of each request (None:
     row i).  A slot outside the pool marks a padding row: 0 in the result, left
     as it was in a given ``out``.  A slot named by several rows takes their
-    tokens in row order."""
+    tokens in row order.  Every row looks through all slots: meant for batches
+    of up to some thousand requests."""
     fn = "gated_step"
     g = _gate(gate)
     f_rs = _operand(f, None, "gated_step: f")
