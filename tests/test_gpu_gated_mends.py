@@ -332,3 +332,14 @@ def test_projection_of_a_sliding_window(rows, step):
     one = torch.ones(max(rows, N), device=DEV)
     y = sgr.int8_projection(x, w, one[:N], x_scale=one[:rows])
     assert torch.equal(y, (x.double() @ w.double().t()).float())
+
+
+# ------------------------------------------------------------- many bounds
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_sequences_in_many_segments(dtype):
+    """More bounds than a block keeps in shared memory, and enough rows that they
+    are cut into segments."""
+    rng = np.random.default_rng(11)
+    rows, D, n = 60000, 24, 5000
+    cu = [4, *sorted(rng.integers(4, rows - 100, n - 1).tolist()), rows - 100]
+    both_directions(dtype, "sigmoid", rng.normal(size=(rows, D)) * 4, cu)
